@@ -5,7 +5,9 @@
 * ``add_norm_backward`` its gradients (the stream's and the weight's);
 * ``rotate``            rotary positions of several axes (t, h, w) on strided q and k heads, and
                         the inverse rotation, which is its gradient;
-* ``swiglu_backward``   gradients of u = silu(h Wg^T) * (h Wu^T): dh, dWg, dWu.
+* ``swiglu_backward``   gradients of u = silu(h Wg^T) * (h Wu^T): dh, dWg, dWu;
+* ``matvec``            1 to 8 bf16 rows times 4-bit (NVFP4) weights, one projection or the gated
+                        pair of a feed-forward layer.
 
 ``run`` computes a case either in elementary torch operations in 32 bits (own = False) or with
 the library's entry points (own = True); ``exact`` is the definition in 64 bits.
@@ -35,9 +37,6 @@ def listed():
         # two 1024 px samples, FP8 with a scale for each row (the FP8 linears' input)
         {"name": "norm_batch2_1024px_row8", "op": "add_norm", "M": 9216, "D": 4608, "x": "bf16",
          "out": "row8"},
-        # the tiny configuration's fp32 stream, gradients
-        {"name": "norm_backward_tiny_f32", "op": "add_norm_backward", "M": 96, "D": 1024,
-         "x": "f32", "dy": "bf16", "dg": True},
         # one 1024 px sample, all gradients
         {"name": "norm_backward_1024px", "op": "add_norm_backward", "M": 4608, "D": 4608,
          "x": "bf16", "dy": "bf16", "dg": True},
@@ -53,9 +52,6 @@ def listed():
         {"name": "rotate_clip_gradient_f32", "op": "rotate", "B": 1, "T": 77, "gt": 5, "gh": 17,
          "gw": 23, "H": 16, "Hk": 4, "d": 128, "R": 128, "s0": 24, "s1": 20, "s2": 20,
          "x": "f32", "view": "blhd", "interleaved": True, "adjacent": True, "inverse": True},
-        # the tiny configuration, all gradients
-        {"name": "swiglu_backward_tiny", "op": "swiglu_backward", "M": 96, "I": 2816, "K": 1024,
-         "dw": True},
         # a few rows through frozen full-width weights (adapter training on short text)
         {"name": "swiglu_backward_17_rows", "op": "swiglu_backward", "M": 17, "I": 12288,
          "K": 4608, "dw": False},
@@ -65,6 +61,12 @@ def listed():
         # full-width layer at 1024 px, all gradients: the largest
         {"name": "swiglu_backward_1024px", "op": "swiglu_backward", "M": 4608, "I": 12288,
          "K": 4608, "dw": True},
+        # one token through the 4-bit down projection
+        {"name": "matvec_down_one_token", "op": "matvec", "M": 1, "N": 4608, "K": 12288,
+         "gated": False, "out": "bf16"},
+        # eight tokens, one of each sequence of a batch, through the 4-bit gate and up projections
+        {"name": "matvec_gate_up_batch8", "op": "matvec", "M": 8, "N": 12288, "K": 4608,
+         "gated": True, "out": "bf16"},
     ]
 
 
@@ -73,7 +75,7 @@ def _log_int(rng, lo, hi):
 
 
 def draw(rng):
-    op = rng.choice(("add_norm", "add_norm_backward", "rotate", "swiglu_backward"))
+    op = rng.choice(("add_norm", "add_norm_backward", "rotate", "swiglu_backward", "matvec"))
     if op == "add_norm":
         out = rng.choice(("bf16", "f32", "row8", "mx8"))
         D = 128 * _log_int(rng, 1, 64) if out == "mx8" else 8 * _log_int(rng, 1, 1024)
@@ -100,6 +102,11 @@ def draw(rng):
             case["gh"], case["T"], case["B"] = (max(1, case["gh"] // 2), max(1, case["T"] // 2),
                                                 max(1, case["B"] // 2))
         return case
+    if op == "matvec":
+        gated = rng.random() < 0.4
+        return {"op": op, "M": rng.randint(1, 8), "N": _log_int(rng, 16, 16384),
+                "K": 64 * _log_int(rng, 1, 192), "gated": gated,
+                "out": "bf16" if gated else rng.choice(("bf16", "f32"))}
     return {"op": op, "M": _log_int(rng, 1, 4608), "I": 128 * _log_int(rng, 1, 96),
             "K": 64 * _log_int(rng, 2, 72), "dw": rng.random() < 0.75}
 
@@ -131,6 +138,10 @@ def work(case):
         n = _rotate_elements(case)
         pos = 12 * _rotate_len(case) * (case["B"] if case["T"] == 1 and case["gt"] == 0 else 1)
         return {"bytes": 2 * n * _bytes(case["x"]) + pos, "flops": 3 * n * case["R"] // case["d"]}
+    if op == "matvec":
+        M, N, K, two = case["M"], case["N"], case["K"], 1 + case["gated"]
+        return {"bytes": two * N * (K // 2 + K // 16 + 4) + (0 if case["gated"] else 4 * N) +
+                2 * M * K + M * N * _bytes(case["out"]), "flops": 2 * two * M * N * K}
     M, I, K = case["M"], case["I"], case["K"]
     return {"bytes": 2 * (2 * M * K + 2 * I * K + M * I) + (4 * I * K if case["dw"] else 0),
             "flops": 4 * M * I * K * (3 if case["dw"] else 2)}
@@ -158,6 +169,16 @@ def _positions(case, gen):
                              torch.arange(gw, device="cuda"), indexing="ij")
     image = T + torch.stack([t.reshape(-1), h.reshape(-1), w.reshape(-1)])
     return torch.cat([text, image], 1).to(torch.int32).contiguous()
+
+
+def _pack_rows(values):
+    """[rows, groups] one-byte group scales in the tensor cores' order (rows padded to 128, groups
+    to 4, with zero bytes): byte 512 (r/128 * groups/4 + c/4) + 16 (r % 32) + 4 (r % 128 / 32) + c % 4."""
+    n, groups = values.shape
+    rows, cols = -(-n // 128) * 128, -(-groups // 4) * 4
+    full = values.new_zeros(rows, cols)
+    full[:n, :groups] = values
+    return full.view(rows // 128, 4, 32, cols // 4, 4).permute(0, 3, 2, 1, 4).reshape(-1)
 
 
 def prepare(case, seed):
@@ -213,6 +234,21 @@ def prepare(case, seed):
         st["k_out"] = torch.empty_like(st["k"]) if Hk else None
         st["pos"] = _positions(case, gen)
         st["axes"] = torch.tensor(_axes(case), device="cuda")
+    elif op == "matvec":
+        M, N, K = case["M"], case["N"], case["K"]
+        st["x"] = randn(M, K)
+        for name in ("gate", "up") if case["gated"] else ("w",):
+            # two codes a byte; scales of 16-element groups as a quantiser's maxima give them
+            st[name] = torch.randint(0, 256, (N, K // 2), device="cuda", generator=gen,
+                                     dtype=torch.uint8)
+            sf = (torch.exp(randn(N, K // 16, dt=torch.float32, std=0.3)) * 64).clamp(max=448)
+            st[name + "_sf"] = sf.to(torch.float8_e4m3fn)
+            # the same scales in the tensor cores' order, laid out once with the weights
+            st[name + "_packed"] = _pack_rows(st[name + "_sf"].view(torch.uint8))
+            st[name + "_scale"] = torch.exp(randn(N, dt=torch.float32, std=0.2)) * (
+                K ** -0.5 / 192)
+        st["bias"] = None if case["gated"] else randn(N, dt=torch.float32, std=0.5)
+        st["out"] = empty(M, N, dt=_DT[case["out"]])
     else:
         M, I, K = case["M"], case["I"], case["K"]
         st["h"] = randn(M, K)
@@ -279,18 +315,19 @@ def _own_swiglu_backward(st, case):
     return {"dh": st["dh_out"], "dwg": st["dwg_out"], "dwu": st["dwu_out"]}
 
 
+def _own_matvec(st, case):
+    from stream_diffusion_transformer_fwd_b200 import ig4
+    if case["gated"]:
+        ig4.ig4_nvfp4_swiglu_matvec(st["x"], st["gate"], st["gate_packed"], st["gate_scale"],
+                                    st["up"], st["up_packed"], st["up_scale"], st["out"])
+    else:
+        ig4.ig4_nvfp4_matvec(st["x"], st["w"], st["w_packed"], st["w_scale"], st["bias"],
+                             st["out"])
+    return {"out": st["out"]}
+
+
 _OWN = {"add_norm": _own_add_norm, "add_norm_backward": _own_add_norm_backward,
-        "rotate": _own_rotate, "swiglu_backward": _own_swiglu_backward}
-
-
-def _pack_rows(values):
-    """[M, D / 32] block scales in the tensor cores' order (rows padded to 128 with zero bytes):
-    byte 512 (r/128 * D/128 + kb) + 16 (r % 32) + 4 (r % 128 / 32) + block % 4."""
-    M, nb = values.shape
-    rows = -(-M // 128) * 128
-    full = values.new_zeros(rows, nb)
-    full[:M] = values
-    return full.view(rows // 128, 4, 32, nb // 4, 4).permute(0, 3, 2, 1, 4).reshape(-1)
+        "rotate": _own_rotate, "swiglu_backward": _own_swiglu_backward, "matvec": _own_matvec}
 
 
 def _plain_add_norm(st, case):
@@ -361,8 +398,29 @@ def _plain_swiglu_backward(st, case):
     return res
 
 
+_E2M1 = (0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0, -0.0, -0.5, -1.0, -1.5, -2.0, -3.0, -4.0, -6.0)
+
+
+def _plain_project(st, name):
+    """x W^T with W expanded from its codes (element 2i in the low nibble) and scales."""
+    q = st[name].int()
+    codes = torch.stack([q & 15, q >> 4], -1).view(q.shape[0], -1, 16)
+    w = torch.tensor(_E2M1, device="cuda")[codes] * st[name + "_sf"].float()[..., None]
+    return (st["x"].float() @ w.view(q.shape[0], -1).T) * st[name + "_scale"]
+
+
+def _plain_matvec(st, case):
+    if case["gated"]:
+        g = _plain_project(st, "gate")
+        y = g / (1.0 + torch.exp(-g)) * _plain_project(st, "up")
+    else:
+        y = _plain_project(st, "w") + st["bias"]
+    return {"out": y.to(st["out"].dtype)}
+
+
 _PLAIN = {"add_norm": _plain_add_norm, "add_norm_backward": _plain_add_norm_backward,
-          "rotate": _plain_rotate, "swiglu_backward": _plain_swiglu_backward}
+          "rotate": _plain_rotate, "swiglu_backward": _plain_swiglu_backward,
+          "matvec": _plain_matvec}
 
 
 # ------------------------------------------------------- the definition, 64 bits
@@ -417,6 +475,20 @@ def exact(case, seed):
             return out
         pos = st["pos"].double()
         return {"q": turned(st["q"], pos), "k": turned(st["k"], pos)}
+    if op == "matvec":
+        def project(name):
+            q = st[name].long()
+            w = torch.empty(q.shape[0], 2 * q.shape[1], dtype=torch.float64, device="cuda")
+            for side, c in ((0, q % 16), (1, q // 16)):
+                e, m = c % 8 // 2, c % 2  # sign, two exponent bits (bias 1), one mantissa bit
+                size = torch.where(e == 0, 0.5 * m, 2.0 ** (e - 1).double() * (1 + 0.5 * m))
+                w[:, side::2] = torch.where(c >= 8, -size, size)
+            w *= st[name + "_sf"].double().repeat_interleave(16, 1)
+            return st["x"].double().matmul(w.t()) * st[name + "_scale"].double()
+        if case["gated"]:
+            gate = project("gate")
+            return {"out": gate * torch.sigmoid(gate) * project("up")}
+        return {"out": project("w") + st["bias"].double()}
     h, wg, wu, du = (st[n].double() for n in ("h", "wg", "wu", "du"))
     gate, up = h.matmul(wg.t()), h.matmul(wu.t())
     sig = torch.sigmoid(gate)
