@@ -248,6 +248,105 @@ ig4_status ig4_quantize_mx8(int M, int K, const void *x, void *codes_out, void *
                             void *stream);
 size_t ig4_mx8_scale_bytes(int M, int K);
 
+/* ------------------------------------------ residual addition + RMSNorm ---
+ * The pre-norm of a layer whose residual branch ends outside the fused block
+ * (an adapter's sum, a text-side layer in front of ig4_text_cond_project):
+ *   t = x + r,  s = RN(t),  y = t * rsqrt(mean(t^2) + eps) * g,
+ * per row, in fp32; the norm takes the unrounded sum t.  x, r, s_out [M][D] in
+ * x_dtype (F32 or BF16); r NULL: t = x; g fp32 [D], NULL: all ones; s_out NULL:
+ * not wanted.  y_out [M][D] in y_dtype: F32, BF16, or E4M3 with exactly one of
+ *   y_scale_out  fp32 [M]: scale[m] = max|y[m]| / 448 (1 for a zero row), codes
+ *                of y / scale, as ig4_quantize_rows;
+ *   y_sf_out     ig4_mx8_scale_bytes(M, D) bytes: the MX8 form of
+ *                ig4_quantize_mx8 of the bf16-rounded y (padding rows are not
+ *                written); D % 128 == 0.
+ * A row that holds an infinity or a NaN comes out as NaN where y is NaN.
+ * M >= 1, D % 8 == 0, D <= 8192, eps > 0.  s_out may be x or r; otherwise the
+ * outputs overlap neither an input nor one another.  Matrices and g 16-byte
+ * aligned, y_scale_out and y_sf_out 4-byte.  Errors: INVALID_ARG. */
+ig4_status ig4_add_rms_norm(int M, int D, const void *x, const void *r, int x_dtype,
+                            const float *g, float eps, void *s_out, void *y_out, int y_dtype,
+                            float *y_scale_out, void *y_sf_out, void *stream);
+
+/* Gradients of ig4_add_rms_norm at the stored sum s (rounding s and y is taken
+ * as the identity): with rstd = rsqrt(mean(s^2) + eps) and n = s rstd,
+ *   dx = rstd (dy g - n mean(dy g n)) + ds   (the gradient of x and of r),
+ *   dg[d] = sum_m dy[m][d] n[m][d].
+ * s, ds, dx_out [M][D] in s_dtype; dy [M][D] in dy_dtype (F32 or BF16); ds NULL:
+ * no gradient arrives on the stream; dg_out fp32 [D], NULL: a frozen weight.
+ * The row sums of dg are added in a fixed order: the same call gives the same
+ * bits.  workspace (256-byte aligned) of
+ * ig4_add_rms_norm_backward_workspace_size(M, D) bytes, used only with dg_out.
+ * Sizes as for ig4_add_rms_norm (0 bytes if they are invalid); dx_out may be
+ * ds; otherwise outputs and workspace overlap no input and not one another.
+ * Errors: INVALID_ARG, WORKSPACE. */
+size_t ig4_add_rms_norm_backward_workspace_size(int M, int D);
+ig4_status ig4_add_rms_norm_backward(int M, int D, const void *s, int s_dtype, const float *g,
+                                     float eps, const void *dy, int dy_dtype, const void *ds,
+                                     void *dx_out, float *dg_out, void *workspace,
+                                     size_t ws_bytes, void *stream);
+
+/* --------------------------------------------------- MRoPE on q/k heads ---
+ * Rotary positions with several axes (survey page, "单 block 内部": 3D MRoPE)
+ * on heads that the fused QKV projection did not produce (a projection with an
+ * adapter's sum, another head width, a decoded token), and the inverse
+ * rotation, which is the gradient's.  Pair j < R/2 of token (b, l) turns by
+ * pos[b][axis(j)][l] * theta^(-2j/R):
+ *   (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin)     (inverse: sin negated);
+ * elements past the R rotary ones pass through. */
+typedef struct ig4_rotary {
+  int B, L;            /* samples, tokens of each */
+  int head_dim;        /* 2 .. 1024 */
+  int rotary_dim;      /* R: even, <= head_dim, <= 512 */
+  double theta;        /* > 0, finite */
+  int sections[3];     /* pairs of t, h, w: sum R / 2 */
+  int interleaved;     /* 0: axis(j) in contiguous sections t, h, w; 1: the axes in turn
+                          (t, h, w, t, ..), each until its section is used up */
+  int adjacent;        /* 0: pair j joins elements j and j + R/2; 1: 2j and 2j + 1 */
+  int inverse;         /* 0: rotate; 1: rotate back */
+  int dtype;           /* IG4_F32 or IG4_BF16 */
+} ig4_rotary;
+
+/* A strided tensor of heads: element (b, l, h, e) at data[b stride_b + l
+ * stride_l + h stride_h + e] (strides in elements, >= 0). */
+typedef struct ig4_heads {
+  void *data;
+  int H;
+  long long stride_b, stride_l, stride_h;
+} ig4_heads;
+
+/* q (and k, may have another H; both its pointers NULL: absent) -> q_out
+ * (k_out) in one launch.  pos: device int32, axis rows of L, [3][L] of sample b
+ * at pos + b * pos_stride_b (0: all samples share one table, as
+ * ig4_mrope_positions writes it).  Any alignment of the element type and any
+ * strides are taken; rows whose pointers and strides are 16-byte multiples
+ * move fastest.  An output is its own input (same pointer and strides: in
+ * place) or overlaps no input; no two elements of an output coincide.
+ * B, L, H >= 1, B * L < 2^31.  Errors: INVALID_ARG. */
+ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long pos_stride_b,
+                            const ig4_heads *q, const ig4_heads *q_out, const ig4_heads *k,
+                            const ig4_heads *k_out, void *stream);
+
+/* ------------------------------------------------------ SwiGLU gradients ---
+ * Gradients of ig4_swiglu's u = silu(G) * U, G = h W_gate^T, U = h W_up^T (bf16
+ * weights), from du = dL/du:
+ *   dU = du G sig(G),  dG = du U sig(G) (1 + G (1 - sig(G))),
+ *   dh = dG W_gate + dU W_up,  dW_gate = dG^T h,  dW_up = dU^T h.
+ * G and U are recomputed; dG and dU are rounded to bf16 once, as operands of
+ * the products, whose sums are fp32.  All matrices bf16, dense: h, dh_out
+ * [M][K]; w_gate, w_up, dw_gate_out, dw_up_out [I][K]; du [M][I].  dh_out NULL:
+ * not wanted; dw_gate_out and dw_up_out both NULL: frozen weights (not all
+ * three).  M >= 1, I % 128 == 0, K % 64 == 0 (else UNSUPPORTED), M <= 2^20,
+ * I, K <= 2^17.  workspace (256-byte aligned) of
+ * ig4_swiglu_backward_workspace_size(M, I, K) bytes (0 if invalid).  Outputs
+ * and workspace overlap no input and not one another; 16-byte aligned.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE. */
+size_t ig4_swiglu_backward_workspace_size(int M, int I, int K);
+ig4_status ig4_swiglu_backward(int M, int I, int K, const void *h, const void *w_gate,
+                               const void *w_up, const void *du, void *dh_out,
+                               void *dw_gate_out, void *dw_up_out, void *workspace,
+                               size_t ws_bytes, void *stream);
+
 /* --------------------------------------------------------- whole block ---
  * Bytes of workspace ig4_block_forward needs for cfg (0 if cfg is invalid). */
 size_t ig4_workspace_size(const ig4_config *cfg);

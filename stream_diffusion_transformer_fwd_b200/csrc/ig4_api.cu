@@ -15,11 +15,14 @@
 #include <utility>
 
 #include "ig4.h"
+#include "ig4_addnorm.cuh"
 #include "ig4_attention.cuh"
+#include "ig4_ffn_grad.cuh"
 #include "ig4_gemm.cuh"
 #include "ig4_mx8.cuh"
 #include "ig4_nvf4.cuh"
 #include "ig4_parallel.cuh"
+#include "ig4_rotate.cuh"
 #include "ig4_small.cuh"
 
 using namespace ig4;
@@ -2401,6 +2404,452 @@ ig4_status ig4_selftest_timeout(int wait_us, void *stream) {
   selftest_timeout_kernel<<<1, 32, 0, as_stream(stream)>>>(
       static_cast<unsigned long long>(wait_us) * 1000ull);
   return last_launch_status();
+}
+
+}  // extern "C"
+
+// ------------------------------------------- operators beside the block
+// Residual addition + RMSNorm, rotary heads, SwiGLU gradients.
+
+namespace {
+
+struct Span {
+  const void *p;
+  size_t bytes;
+};
+bool overlap(const Span &a, const Span &b) {
+  const uint8_t *x = static_cast<const uint8_t *>(a.p), *y = static_cast<const uint8_t *>(b.p);
+  return x && y && x < y + b.bytes && y < x + a.bytes;
+}
+// No output may touch an input or another output; an output that starts at an
+// input its entry in `own` names is that input, in place.
+bool spans_ok(const Span *in, int n_in, const Span *out, int n_out, bool (*own)(int, int)) {
+  for (int o = 0; o < n_out; ++o) {
+    for (int i = 0; i < n_in; ++i)
+      if (overlap(in[i], out[o]) && !(own(o, i) && in[i].p == out[o].p)) return false;
+    for (int q = o + 1; q < n_out; ++q)
+      if (overlap(out[o], out[q])) return false;
+  }
+  return true;
+}
+
+inline size_t esize_of(int dt) { return dt == IG4_F32 ? 4 : (dt == IG4_BF16 ? 2 : 1); }
+
+// ---- add + RMSNorm
+
+bool addnorm_sizes_ok(int M, int D) { return M >= 1 && D >= 8 && D % 8 == 0 && D <= 8192; }
+
+// Launch shape: a warp per row up to ADDNORM_WARP_D, else a CTA of as many
+// warps as cover the row with ADDNORM_NV vectors per thread; `per_sm` CTAs on
+// each SM walk the rows.
+struct AddNormPlan {
+  bool warp;
+  int threads, grid;
+};
+AddNormPlan addnorm_plan(int M, int D, int sms, int threads_per_sm) {
+  AddNormPlan p{};
+  p.warp = D <= ADDNORM_WARP_D;
+  const int nvec = D / 8;
+  p.threads = p.warp ? 32 * ADDNORM_WARPS : 32 * ((nvec + 32 * ADDNORM_NV - 1) / (32 * ADDNORM_NV));
+  const long rows = p.warp ? (M + ADDNORM_WARPS - 1L) / ADDNORM_WARPS : M;
+  const int per_sm = std::max(1, threads_per_sm / p.threads);
+  p.grid = static_cast<int>(std::min<long>(rows, static_cast<long>(sms) * per_sm));
+  return p;
+}
+constexpr int ADDNORM_FWD_THREADS_PER_SM = 1024;
+constexpr int ADDNORM_BWD_THREADS_PER_SM = 576;
+constexpr int ADDNORM_MAX_SMS = 160;  // bounds the partial rows of dg in the workspace
+
+template <typename XT, int OUT>
+ig4_status launch_add_norm_t(int M, int D, const void *x, const void *r, const float *g, float eps,
+                             void *s, void *y, float *scale, void *sf, cudaStream_t st) {
+  DeviceInfo *di = nullptr;
+  IG4_TRY(device_info(&di));
+  const AddNormPlan p = addnorm_plan(M, D, di->sms, ADDNORM_FWD_THREADS_PER_SM);
+  const XT *xp = static_cast<const XT *>(x), *rp = static_cast<const XT *>(r);
+  XT *sp = static_cast<XT *>(s);
+  uint8_t *sfp = static_cast<uint8_t *>(sf);
+  const cudaError_t e =
+      p.warp ? launch_pdl(add_rms_norm_kernel<XT, OUT, ADDNORM_NV, true>, dim3(p.grid),
+                          dim3(p.threads), 0, st, xp, rp, g, eps, sp, y, scale, sfp, M, D)
+             : launch_pdl(add_rms_norm_kernel<XT, OUT, ADDNORM_NV, false>, dim3(p.grid),
+                          dim3(p.threads), 0, st, xp, rp, g, eps, sp, y, scale, sfp, M, D);
+  return e == cudaSuccess ? last_launch_status() : IG4_ERR_CUDA;
+}
+
+template <typename XT>
+ig4_status launch_add_norm(int out, int M, int D, const void *x, const void *r, const float *g,
+                           float eps, void *s, void *y, float *scale, void *sf, cudaStream_t st) {
+  switch (out) {
+    case ADDNORM_BF16:
+      return launch_add_norm_t<XT, ADDNORM_BF16>(M, D, x, r, g, eps, s, y, scale, sf, st);
+    case ADDNORM_F32:
+      return launch_add_norm_t<XT, ADDNORM_F32>(M, D, x, r, g, eps, s, y, scale, sf, st);
+    case ADDNORM_ROW8:
+      return launch_add_norm_t<XT, ADDNORM_ROW8>(M, D, x, r, g, eps, s, y, scale, sf, st);
+    default:
+      return launch_add_norm_t<XT, ADDNORM_MX8>(M, D, x, r, g, eps, s, y, scale, sf, st);
+  }
+}
+
+template <typename XT, typename YT>
+ig4_status launch_add_norm_grad(int M, int D, const void *s, const float *g, float eps,
+                                const void *dy, const void *ds, void *dx, float *dg, float *part,
+                                cudaStream_t st) {
+  DeviceInfo *di = nullptr;
+  IG4_TRY(device_info(&di));
+  const AddNormPlan p =
+      addnorm_plan(M, D, std::min(di->sms, ADDNORM_MAX_SMS), ADDNORM_BWD_THREADS_PER_SM);
+  float *pp = dg ? part : nullptr;
+  const XT *sp = static_cast<const XT *>(s), *dsp = static_cast<const XT *>(ds);
+  const YT *dyp = static_cast<const YT *>(dy);
+  XT *dxp = static_cast<XT *>(dx);
+  const cudaError_t e =
+      p.warp ? launch_pdl(add_rms_norm_grad_kernel<XT, YT, ADDNORM_NV, true>, dim3(p.grid),
+                          dim3(p.threads), 0, st, sp, g, eps, dyp, dsp, dxp, pp, M, D)
+             : launch_pdl(add_rms_norm_grad_kernel<XT, YT, ADDNORM_NV, false>, dim3(p.grid),
+                          dim3(p.threads), 0, st, sp, g, eps, dyp, dsp, dxp, pp, M, D);
+  if (e != cudaSuccess) return IG4_ERR_CUDA;
+  IG4_TRY(last_launch_status());
+  if (!dg) return IG4_OK;
+  if (launch_pdl(add_rms_norm_dg_kernel, dim3((D + 31) / 32), dim3(ADDNORM_DG_THREADS), 0, st,
+                 static_cast<const float *>(part), p.grid, D, dg) != cudaSuccess)
+    return IG4_ERR_CUDA;
+  return last_launch_status();
+}
+
+// ---- rotary heads
+
+// Whether no two elements of the [B][L][H][d] tensor coincide: sorted by
+// stride, each dimension's step clears the extent of those inside it.
+bool heads_distinct(const ig4_heads &t, int B, int L, int d) {
+  struct Dim {
+    long long n, s;
+  } dim[3] = {{B, t.stride_b}, {L, t.stride_l}, {t.H, t.stride_h}};
+  std::sort(dim, dim + 3, [](const Dim &a, const Dim &b) { return a.s < b.s; });
+  long long extent = d;
+  for (const Dim &q : dim) {
+    if (q.n == 1) continue;
+    if (q.s < extent) return false;
+    extent += (q.n - 1) * q.s;
+  }
+  return true;
+}
+bool heads_ok(const ig4_heads &t, int esize) {
+  constexpr long long MAX_STRIDE = 1LL << 40;
+  return t.data && t.H >= 1 && t.H <= (1 << 20) && t.stride_b >= 0 && t.stride_l >= 0 &&
+         t.stride_h >= 0 && t.stride_b < MAX_STRIDE && t.stride_l < MAX_STRIDE &&
+         t.stride_h < MAX_STRIDE && reinterpret_cast<uintptr_t>(t.data) % esize == 0;
+}
+bool heads_vec(const ig4_heads &t, int V, int esize) {
+  return reinterpret_cast<uintptr_t>(t.data) % (V * esize) == 0 && t.stride_b % V == 0 &&
+         t.stride_l % V == 0 && t.stride_h % V == 0;
+}
+
+template <typename T, int V>
+ig4_status launch_rotate_v(const RotateArgs &a, bool adjacent, dim3 grid, cudaStream_t st) {
+  const cudaError_t e =
+      adjacent ? launch_pdl(mrope_rotate_kernel<T, V, true>, grid, dim3(ROTATE_THREADS), 0, st, a)
+               : launch_pdl(mrope_rotate_kernel<T, V, false>, grid, dim3(ROTATE_THREADS), 0, st, a);
+  return e == cudaSuccess ? last_launch_status() : IG4_ERR_CUDA;
+}
+
+// ---- SwiGLU gradients
+
+// MN-major operand (see ig4_ffn_grad.cuh): bf16 matrix [rows][cols], rows the
+// contraction, as slabs of 64 columns; box 64 columns x 64 rows x 2 slabs.
+ig4_status map_mn_slabs(CUtensorMap *m, const void *base, long rows, long cols) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return IG4_ERR_CUDA;
+  cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, 128};
+  cuuint32_t box[3] = {64, 64, 2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? IG4_OK
+             : IG4_ERR_CUDA;
+}
+
+bool swiglu_grad_sizes_ok(int M, int I, int K) {
+  return M >= 1 && M <= (1 << 20) && I >= 128 && I % 128 == 0 && I <= (1 << 17) && K >= 64 &&
+         K % 64 == 0 && K <= (1 << 17);
+}
+
+// Shares of dh's contraction.  With few output tiles most of the 74 CTA pairs
+// would idle, so the 2I-long contraction is cut into equal shares whose fp32
+// partial sums are added afterwards; a share costs the write and the read of
+// one fp32 M x K matrix.  Both sides in units of one k-block of a pair tile
+// (0.28 us): rounds * k-blocks of a share + 8 M K bytes per share at 5 TB/s.
+int swiglu_grad_shares(int M, int I, int K) {
+  const long tiles = static_cast<long>((M + 255) / 256) * ((K + 255) / 256);
+  const int kblocks = 2 * I / 64;
+  int best = 1;
+  double best_cost = 1e300;
+  for (int z = 1; z <= 16 && z <= kblocks; ++z) {
+    const long rounds = (tiles * z + 73) / 74;
+    const double cost = static_cast<double>(rounds) * ((kblocks + z - 1) / z + 4) +
+                        (z > 1 ? z * 8.0 * M * K / 1.4e6 + 10 : 0.0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = z;
+    }
+  }
+  return best;
+}
+
+struct SwigluGradWs {
+  __nv_bfloat16 *p;  // dG | dU [M][2I]
+  float *part;       // [shares][M][K]
+  size_t bytes;
+};
+SwigluGradWs swiglu_grad_ws(int M, int I, int K, void *base) {
+  SwigluGradWs w{};
+  uint8_t *b = static_cast<uint8_t *>(base);
+  const size_t pb = round_up(static_cast<size_t>(M) * 2 * I * 2, 256);
+  const int z = swiglu_grad_shares(M, I, K);
+  w.p = reinterpret_cast<__nv_bfloat16 *>(b);
+  w.part = z > 1 ? reinterpret_cast<float *>(b + pb) : nullptr;
+  w.bytes = pb + (z > 1 ? round_up(static_cast<size_t>(z) * M * K * 4, 256) : 0);
+  return w;
+}
+
+template <bool A_MN>
+ig4_status launch_grad_gemm(const CUtensorMap &A, const CUtensorMap &B0, const CUtensorMap &B1,
+                            long rows, int N, int kblocks, int kb0, int shares, int group_m,
+                            const EpiGrad &epi, cudaStream_t st) {
+  DeviceInfo *di = nullptr;
+  IG4_TRY(device_info(&di));
+  auto kern = grad_pair_kernel<A_MN>;
+  IG4_TRY(allow_smem(kern, GRAD_SMEM_BYTES));
+  const int m_tiles = static_cast<int>((rows + 255) / 256), n_tiles = (N + 255) / 256;
+  const long items = static_cast<long>(m_tiles) * n_tiles * shares;
+  const int pairs = static_cast<int>(std::min<long>(items, di->sms / 2));
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(2 * pairs);
+  lc.blockDim = dim3(GEMM_THREADS);
+  lc.dynamicSmemBytes = GRAD_SMEM_BYTES;
+  lc.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = attr;
+  lc.numAttrs = 2;
+  if (cudaLaunchKernelEx(&lc, kern, A, B0, B1, m_tiles, n_tiles, kblocks, kb0, shares, group_m,
+                         epi) != cudaSuccess)
+    return IG4_ERR_CUDA;
+  return last_launch_status();
+}
+
+}  // namespace
+
+extern "C" {
+
+ig4_status ig4_add_rms_norm(int M, int D, const void *x, const void *r, int x_dtype,
+                            const float *g, float eps, void *s_out, void *y_out, int y_dtype,
+                            float *y_scale_out, void *y_sf_out, void *stream) {
+  if (!addnorm_sizes_ok(M, D) || !x || !y_out || !(eps > 0.0f)) return IG4_ERR_INVALID_ARG;
+  if (!valid_dtype_x(x_dtype) || (!valid_dtype_x(y_dtype) && y_dtype != IG4_E4M3))
+    return IG4_ERR_INVALID_ARG;
+  const bool f8 = y_dtype == IG4_E4M3;
+  if (f8 ? (!y_scale_out == !y_sf_out) : (y_scale_out || y_sf_out)) return IG4_ERR_INVALID_ARG;
+  if (y_sf_out && D % 128) return IG4_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(r) || !aligned16(g) || !aligned16(s_out) || !aligned16(y_out) ||
+      reinterpret_cast<uintptr_t>(y_scale_out) % 4 || reinterpret_cast<uintptr_t>(y_sf_out) % 4)
+    return IG4_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(M) * D, xb = n * esize_of(x_dtype);
+  const Span in[] = {{x, xb}, {r, xb}, {g, static_cast<size_t>(D) * 4}};
+  const Span out[] = {{s_out, xb},
+                      {y_out, n * esize_of(y_dtype)},
+                      {y_scale_out, static_cast<size_t>(M) * 4},
+                      {y_sf_out, y_sf_out ? mx8_sf_bytes(M, D) : 0}};
+  if (!spans_ok(in, 3, out, 4, [](int o, int i) { return o == 0 && i < 2; }))
+    return IG4_ERR_INVALID_ARG;
+  const int kind = f8 ? (y_sf_out ? ADDNORM_MX8 : ADDNORM_ROW8)
+                      : (y_dtype == IG4_BF16 ? ADDNORM_BF16 : ADDNORM_F32);
+  return x_dtype == IG4_F32
+             ? launch_add_norm<float>(kind, M, D, x, r, g, eps, s_out, y_out, y_scale_out, y_sf_out,
+                                      as_stream(stream))
+             : launch_add_norm<__nv_bfloat16>(kind, M, D, x, r, g, eps, s_out, y_out, y_scale_out,
+                                              y_sf_out, as_stream(stream));
+}
+
+size_t ig4_add_rms_norm_backward_workspace_size(int M, int D) {
+  if (!addnorm_sizes_ok(M, D)) return 0;
+  const AddNormPlan p = addnorm_plan(M, D, ADDNORM_MAX_SMS, ADDNORM_BWD_THREADS_PER_SM);
+  return round_up(static_cast<size_t>(p.grid) * D * 4, 256);
+}
+
+ig4_status ig4_add_rms_norm_backward(int M, int D, const void *s, int s_dtype, const float *g,
+                                     float eps, const void *dy, int dy_dtype, const void *ds,
+                                     void *dx_out, float *dg_out, void *workspace,
+                                     size_t ws_bytes, void *stream) {
+  if (!addnorm_sizes_ok(M, D) || !s || !dy || !dx_out || !(eps > 0.0f)) return IG4_ERR_INVALID_ARG;
+  if (!valid_dtype_x(s_dtype) || !valid_dtype_x(dy_dtype)) return IG4_ERR_INVALID_ARG;
+  if (!aligned16(s) || !aligned16(g) || !aligned16(dy) || !aligned16(ds) || !aligned16(dx_out) ||
+      reinterpret_cast<uintptr_t>(dg_out) % 4)
+    return IG4_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(M) * D, db = static_cast<size_t>(D) * 4;
+  const size_t need = dg_out ? ig4_add_rms_norm_backward_workspace_size(M, D) : 0;
+  if (need && (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+    return IG4_ERR_WORKSPACE;
+  const size_t sb = n * esize_of(s_dtype);
+  const Span in[] = {{ds, sb}, {s, sb}, {dy, n * esize_of(dy_dtype)}, {g, db}};
+  const Span out[] = {{dx_out, sb}, {dg_out, db}, {need ? workspace : nullptr, need}};
+  if (!spans_ok(in, 4, out, 3, [](int o, int i) { return o == 0 && i == 0; }))
+    return IG4_ERR_INVALID_ARG;
+  float *part = static_cast<float *>(workspace);
+  cudaStream_t st = as_stream(stream);
+  using bf = __nv_bfloat16;
+  if (s_dtype == IG4_F32)
+    return dy_dtype == IG4_F32
+               ? launch_add_norm_grad<float, float>(M, D, s, g, eps, dy, ds, dx_out, dg_out, part, st)
+               : launch_add_norm_grad<float, bf>(M, D, s, g, eps, dy, ds, dx_out, dg_out, part, st);
+  return dy_dtype == IG4_F32
+             ? launch_add_norm_grad<bf, float>(M, D, s, g, eps, dy, ds, dx_out, dg_out, part, st)
+             : launch_add_norm_grad<bf, bf>(M, D, s, g, eps, dy, ds, dx_out, dg_out, part, st);
+}
+
+ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long pos_stride_b,
+                            const ig4_heads *q, const ig4_heads *q_out, const ig4_heads *k,
+                            const ig4_heads *k_out, void *stream) {
+  if (!rot || !pos || !q || !q_out || !k != !k_out) return IG4_ERR_INVALID_ARG;
+  const int B = rot->B, L = rot->L, d = rot->head_dim, R = rot->rotary_dim;
+  if (B < 1 || L < 1 || static_cast<long>(B) * L >= (1L << 31) || d < 2 || d > 1024 || R < 2 ||
+      R % 2 || R > d || R > 2 * ROTATE_MAX_PAIRS || !(rot->theta > 0.0) || std::isinf(rot->theta) ||
+      !valid_dtype_x(rot->dtype) || pos_stride_b < 0 ||
+      reinterpret_cast<uintptr_t>(pos) % 4)
+    return IG4_ERR_INVALID_ARG;
+  int left[3];
+  long pairs = 0;
+  for (int a = 0; a < 3; ++a) {
+    if (rot->sections[a] < 0) return IG4_ERR_INVALID_ARG;
+    pairs += left[a] = rot->sections[a];
+  }
+  if (pairs != R / 2) return IG4_ERR_INVALID_ARG;
+  const int es = static_cast<int>(esize_of(rot->dtype));
+  RotateArgs a{};
+  const ig4_heads *ins[2] = {q, k}, *outs[2] = {q_out, k_out};
+  int V = 16 / es;
+  // whole vectors in both halves of a head and past the rotary elements
+  const int half = rot->adjacent ? R : R / 2;
+  if (half % V || (d - R) % V) V = 1;
+  int heads = 0;
+  for (int w = 0; w < 2; ++w) {
+    if (!ins[w]) continue;
+    const ig4_heads &i = *ins[w], &o = *outs[w];
+    if (!heads_ok(i, es) || !heads_ok(o, es) || i.H != o.H || !heads_distinct(o, B, L, d))
+      return IG4_ERR_INVALID_ARG;
+    if (i.data == o.data &&
+        (i.stride_b != o.stride_b || i.stride_l != o.stride_l || i.stride_h != o.stride_h))
+      return IG4_ERR_INVALID_ARG;
+    if (!heads_vec(i, V, es) || !heads_vec(o, V, es)) V = 1;
+    a.t[w] = {i.data, o.data, i.H, i.stride_b, i.stride_l, i.stride_h,
+              o.stride_b, o.stride_l, o.stride_h};
+    heads += i.H;
+  }
+  if (k_out && k_out->data == q_out->data) return IG4_ERR_INVALID_ARG;
+  for (int j = 0, turn = 0; j < R / 2; ++j) {
+    if (!rot->interleaved) turn = 0;
+    while (left[turn] == 0) turn = (turn + 1) % 3;
+    --left[turn];
+    a.axis[j / 16] |= static_cast<uint32_t>(turn) << (2 * (j % 16));
+    if (rot->interleaved) turn = (turn + 1) % 3;
+  }
+  DeviceInfo *di = nullptr;
+  IG4_TRY(device_info(&di));
+  a.pos = pos;
+  a.pos_b = pos_stride_b;
+  a.B = B;
+  a.L = L;
+  a.d = d;
+  a.R = R;
+  a.log2_theta = std::log2(rot->theta);
+  a.sin_sign = rot->inverse ? -1.0f : 1.0f;
+  // Tokens per CTA: as many as keep 4 CTAs for every SM, up to 4 and to the
+  // table's size; with fewer tokens than that the heads are shared out too.
+  const long ntok = static_cast<long>(B) * L, want = 4L * di->sms;
+  a.tt = static_cast<int>(std::max<long>(
+      1, std::min<long>({4, ROTATE_TABLE / (R / 2), ntok / want})));
+  const long tiles = (ntok + a.tt - 1) / a.tt;
+  a.hs = static_cast<int>(std::max<long>(1, std::min<long>({heads, 64, want / tiles})));
+  const dim3 grid(static_cast<unsigned>(tiles), a.hs);
+  cudaStream_t st = as_stream(stream);
+  const bool adj = rot->adjacent != 0;
+  if (rot->dtype == IG4_F32)
+    return V > 1 ? launch_rotate_v<float, 4>(a, adj, grid, st)
+                 : launch_rotate_v<float, 1>(a, adj, grid, st);
+  return V > 1 ? launch_rotate_v<__nv_bfloat16, 8>(a, adj, grid, st)
+               : launch_rotate_v<__nv_bfloat16, 1>(a, adj, grid, st);
+}
+
+size_t ig4_swiglu_backward_workspace_size(int M, int I, int K) {
+  return swiglu_grad_sizes_ok(M, I, K) ? swiglu_grad_ws(M, I, K, nullptr).bytes : 0;
+}
+
+ig4_status ig4_swiglu_backward(int M, int I, int K, const void *h, const void *w_gate,
+                               const void *w_up, const void *du, void *dh_out,
+                               void *dw_gate_out, void *dw_up_out, void *workspace,
+                               size_t ws_bytes, void *stream) {
+  if (M < 1 || I < 1 || K < 1 || !h || !w_gate || !w_up || !du || !dw_gate_out != !dw_up_out ||
+      (!dh_out && !dw_gate_out))
+    return IG4_ERR_INVALID_ARG;
+  if (!swiglu_grad_sizes_ok(M, I, K)) return IG4_ERR_UNSUPPORTED;
+  if (!aligned16(h) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(du) ||
+      !aligned16(dh_out) || !aligned16(dw_gate_out) || !aligned16(dw_up_out))
+    return IG4_ERR_INVALID_ARG;
+  const SwigluGradWs ws = swiglu_grad_ws(M, I, K, workspace);
+  if (!workspace || ws_bytes < ws.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255))
+    return IG4_ERR_WORKSPACE;
+  const size_t hb = static_cast<size_t>(M) * K * 2, wb = static_cast<size_t>(I) * K * 2;
+  const Span in[] = {{h, hb}, {w_gate, wb}, {w_up, wb}, {du, static_cast<size_t>(M) * I * 2}};
+  const Span out[] = {{dh_out, hb}, {dw_gate_out, wb}, {dw_up_out, wb}, {workspace, ws.bytes}};
+  if (!spans_ok(in, 4, out, 4, [](int, int) { return false; })) return IG4_ERR_INVALID_ARG;
+  cudaStream_t st = as_stream(stream);
+  {
+    CUtensorMap ma, mg, mu;
+    IG4_TRY(map_2d(&ma, h, 2, M, K, K, GEMM_BM, 64));
+    IG4_TRY(map_2d(&mg, w_gate, 2, I, K, K, 128, 64));
+    IG4_TRY(map_2d(&mu, w_up, 2, I, K, K, 128, 64));
+    const EpiSwiGLUGrad e{static_cast<const __nv_bfloat16 *>(du), ws.p, I, M};
+    IG4_TRY((launch_gemm<256, false, true>(ma, mg, mu, M, I / 128, K, e, st)));
+  }
+  if (dh_out) {
+    const int shares = swiglu_grad_shares(M, I, K);
+    CUtensorMap ma, mg, mu;
+    IG4_TRY(map_2d(&ma, ws.p, 2, M, 2L * I, 2L * I, GEMM_BM, 64));
+    IG4_TRY(map_mn_slabs(&mg, w_gate, I, K));
+    IG4_TRY(map_mn_slabs(&mu, w_up, I, K));
+    const EpiGrad e{static_cast<__nv_bfloat16 *>(dh_out), nullptr, M,
+                    shares > 1 ? ws.part : nullptr, M, K};
+    IG4_TRY(launch_grad_gemm<false>(ma, mg, mu, M, K, 2 * I / 64, I / 64, shares,
+                                    gemm_group_m(M, 2L * I, 2), e, st));
+    if (shares > 1) {
+      const long n8 = static_cast<long>(M) * K / 8;
+      const int grid = static_cast<int>(std::min<long>((n8 + 255) / 256, 148 * 8));
+      if (launch_pdl(grad_reduce_kernel, dim3(grid), dim3(256), 0, st,
+                     reinterpret_cast<const float4 *>(ws.part), shares, n8,
+                     static_cast<uint4 *>(dh_out)) != cudaSuccess)
+        return IG4_ERR_CUDA;
+      IG4_TRY(last_launch_status());
+    }
+  }
+  if (dw_gate_out) {
+    const int kblocks = (M + 63) / 64;
+    CUtensorMap ma, mb;
+    IG4_TRY(map_mn_slabs(&ma, ws.p, M, 2L * I));
+    IG4_TRY(map_mn_slabs(&mb, h, M, K));
+    const EpiGrad e{static_cast<__nv_bfloat16 *>(dw_gate_out),
+                    static_cast<__nv_bfloat16 *>(dw_up_out), I, nullptr, 2 * I, K};
+    IG4_TRY(launch_grad_gemm<true>(ma, mb, mb, 2L * I, K, kblocks, kblocks, 1,
+                                   gemm_group_m(2L * I, M, 2), e, st));
+  }
+  return IG4_OK;
 }
 
 }  // extern "C"

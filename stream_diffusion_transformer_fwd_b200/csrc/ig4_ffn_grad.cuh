@@ -1,0 +1,305 @@
+// ig4_ffn_grad.cuh - gradients of the SwiGLU hidden state
+// u = silu(G) * U, G = h Wg^T, U = h Wu^T, for sm_100a.
+//
+//   dU = du G sig(G),  dG = du U sig(G) (1 + G (1 - sig(G)))
+//   dh = dG Wg + dU Wu,   dWg = dG^T h,   dWu = dU^T h
+//
+// Three tensor-core GEMMs of 4 M I K flops each.  The first recomputes G and U
+// (the forward keeps neither: 4 M I bytes saved per layer) on the forward's
+// dual-B tiles; its epilogue turns the two fp32 accumulators and du into dG
+// and dU and stores them side by side as P [M][2I] in bf16, the type the next
+// two GEMMs' tensor-core operands have (one rounding of 2^-9 relative per
+// factor, as the forward rounds u).  dh contracts P with [Wg; Wu] over 2I in
+// one fp32 accumulator; dW contracts P with h over the tokens.
+//
+// Both later GEMMs contract over a dimension that is not contiguous in
+// memory: the rows of W for dh, the tokens for dW.  tcgen05 reads such
+// operands directly in MN-major form (64 contiguous elements by 8 contraction
+// rows per 128-byte-swizzled 1 KB atom), so nothing is transposed in memory.
+// Tokens past M read as zero from the TMA loads and add nothing.
+#pragma once
+
+#include "ig4_gemm.cuh"
+#include "ig4_ptx.cuh"
+
+namespace ig4 {
+
+// Shared-memory descriptor of an MN-major operand in the 128-byte-swizzle
+// layout: slabs of 64 MN-elements (128 bytes) by 64 contraction rows, 8 KB
+// apart (leading offset), 8-row groups 1 KB apart (stride offset).  One K = 16
+// step starts 16 rows (2 KB) further on.
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192u >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// idesc_bf16 with A and / or B MN-major (bits 15, 16)
+__host__ __device__ constexpr uint32_t idesc_bf16_major(int M, int N, bool a_mn, bool b_mn) {
+  return idesc_bf16(M, N) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
+}
+
+// Epilogue of the recomputation: accumulator columns [0,128) hold G, [128,256)
+// hold U of output columns n .. n + 127; writes dG to p[row][n..] and dU to
+// p[row][I + n..].
+struct EpiSwiGLUGrad {
+  const __nv_bfloat16 *du;
+  __nv_bfloat16 *p;
+  int I, M;
+
+  __device__ __forceinline__ void operator()(int m0, int n0, uint32_t tacc, int r) const {
+    const int row = m0 + r;
+    const bool valid = row < M;
+    const int n = n0 / 2;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      float g[32], up[32];
+      tmem_ld32(tacc + c, g);
+      tmem_ld32(tacc + 128 + c, up);
+      tmem_ld_wait();
+      if (!valid) continue;
+      float d[32];
+      load32_bf16(du + static_cast<long>(row) * I + n + c, d);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float sig = 1.0f / (1.0f + __expf(-g[i]));
+        const float a = d[i] * sig;
+        const float dg = a * up[i] * fmaf(g[i], 1.0f - sig, 1.0f);
+        up[i] = a * g[i];
+        g[i] = dg;
+      }
+      __nv_bfloat16 *dst = p + static_cast<long>(row) * 2 * I + n + c;
+      store32_bf16(dst, g);
+      store32_bf16(dst + I, up);
+    }
+  }
+};
+
+// Output of the two gradient GEMMs: bf16 rows, rows at or past `split_row` in
+// a second matrix (dWg | dWu), or fp32 partial sums of contraction share z.
+struct EpiGrad {
+  __nv_bfloat16 *out0, *out1;
+  int split_row;
+  float *part;  // != nullptr: [shares][rows][N] fp32 partial sums instead
+  int rows, N;
+
+  __device__ __forceinline__ void operator()(int m0, int n0, int z, uint32_t tacc, int r) const {
+    const int row = m0 + r;
+    const bool valid = row < rows;
+    __nv_bfloat16 *o = row < split_row ? out0 + static_cast<long>(row) * N
+                                       : out1 + static_cast<long>(row - split_row) * N;
+    float *pf = part + (static_cast<long>(z) * rows + row) * N;
+#pragma unroll 1
+    for (int c = 0; c < 256; c += 32) {
+      float v[32];
+      tmem_ld32(tacc + c, v);
+      tmem_ld_wait();
+      if (!valid || n0 + c >= N) continue;
+      if (part != nullptr)
+        store32_f32(pf + n0 + c, v);
+      else
+        store32_bf16(o + n0 + c, v);
+    }
+  }
+};
+
+// C = A B on CTA pairs, B MN-major, A K-major (dh) or MN-major (dW).
+// A K-major: tmA maps A [rows][contraction] in boxes of 128 rows x 64; MN-major
+// operands: 3-D maps {64 elements, contraction rows, slabs of 64 elements} in
+// boxes {64, 64, 2}.  The contraction runs over tmB0 for the first kb0 k-blocks
+// and over tmB1 after them.  An item is an output tile of 256 x 256 and one of
+// `shares` equal runs of k-blocks; pairs take items round-robin.  Roles,
+// barriers and the two TMEM accumulators are those of gemm_pair_kernel.
+constexpr int GRAD_STAGES = 6;
+constexpr int GRAD_STAGE_BYTES = 2 * 16384;
+constexpr int GRAD_SMEM_BYTES = GRAD_STAGES * GRAD_STAGE_BYTES + 1024 + 256;
+
+template <bool A_MN>
+__global__ void __launch_bounds__(GEMM_THREADS, 1)
+    grad_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
+                     const __grid_constant__ CUtensorMap tmB1, int m_tiles, int n_tiles, int kblocks,
+                     int kb0, int shares, int group_m, const EpiGrad epi) {
+  constexpr uint32_t IDESC = idesc_bf16_major(2 * GEMM_BM, 256, A_MN, true);
+  constexpr uint32_t TMEM_COLS = 512;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align1024(smem_raw);
+  uint8_t *sA = smem;
+  uint8_t *sB = smem + GRAD_STAGES * 16384;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + GRAD_STAGES * GRAD_STAGE_BYTES);
+  uint64_t *empty = full + GRAD_STAGES;
+  uint64_t *tfull = empty + GRAD_STAGES;
+  uint64_t *tempty = tfull + 2;
+  uint64_t *drain = tempty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1;
+  const int n_pairs = gridDim.x >> 1;
+  const int tiles = m_tiles * n_tiles;
+  const int items = tiles * shares;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < GRAD_STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB0);
+    tma_prefetch_desc(&tmB1);
+  }
+  if (warp == 5) {
+    tmem_alloc_pair(tmem_slot, TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  // k-blocks [first, last) of share z (none empty: shares <= kblocks)
+  auto share_begin = [&](int z) { return static_cast<int>(static_cast<long>(kblocks) * z / shares); };
+
+  if (warp == 4) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      int local = 0;
+      for (int t = pair; t < items && ok; t += n_pairs, ++local) {
+        int mt, nt;
+        const int z = t / tiles;
+        tile_coords(t - z * tiles, m_tiles, n_tiles, group_m, &mt, &nt);
+        const int b0 = share_begin(z), nkb = share_begin(z + 1) - b0;
+        for (int it = 0; it < nkb; ++it) {
+          const int kb = b0 + ((local & 1) ? nkb - 1 - it : it);  // K-snake
+          if (!mbar_wait_cluster(&empty[s], ph ^ 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * GRAD_STAGE_BYTES);
+          const uint32_t bar = map_shared_to_rank(&full[s], 0);
+          const int am = mt * 2 * GEMM_BM + static_cast<int>(rank) * GEMM_BM;
+          if constexpr (A_MN)
+            tma_load_3d_pair(sA + s * 16384, &tmA, bar, 0, kb * 64, am / 64);
+          else
+            tma_load_2d_pair(sA + s * 16384, &tmA, bar, kb * 64, am);
+          const int bn = (nt * 256 + static_cast<int>(rank) * 128) / 64;
+          if (kb < kb0)
+            tma_load_3d_pair(sB + s * 16384, &tmB0, bar, 0, kb * 64, bn);
+          else
+            tma_load_3d_pair(sB + s * 16384, &tmB1, bar, 0, (kb - kb0) * 64, bn);
+          if (++s == GRAD_STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok) sleep_ns(50000);  // let the loads already issued land
+    }
+  } else if (warp == 5) {
+    if (lane == 0 && rank == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      int local = 0;
+      bool ok = true;
+      for (int t = pair; t < items && ok; t += n_pairs, ++local) {
+        const int buf = local & 1;
+        const uint32_t use = static_cast<uint32_t>(local >> 1);
+        if (!mbar_wait_cluster(&tempty[buf], (use & 1) ^ 1, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + buf * 256;
+        const int z = t / tiles;
+        const int nkb = share_begin(z + 1) - share_begin(z);
+        for (int it = 0; it < nkb; ++it) {
+          if (!mbar_wait_cluster(&full[s], ph, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(sA + s * 16384);
+          const uint32_t b_base = smem_u32(sB + s * 16384);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t ad = A_MN ? sdesc_mnmajor_sw128(a_base + kk * 2048)
+                                     : sdesc_kmajor_sw128(a_base + kk * 32);
+            const uint64_t bd = sdesc_mnmajor_sw128(b_base + kk * 2048);
+            umma_bf16_pair(d_tmem, ad, bd, IDESC, (it | kk) != 0);
+          }
+          umma_commit_pair_both(&empty[s]);
+          if (++s == GRAD_STAGES) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) umma_commit_pair_both(&tfull[buf]);
+      }
+      umma_commit_pair_both(drain);
+      mbar_wait_cluster(drain, 0, nullptr, WAIT_LIMIT_NS / 4);
+    }
+  } else {
+    const int r = warp * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t tempty_leader0 = map_shared_to_rank(&tempty[0], 0);
+    const uint32_t tempty_leader1 = map_shared_to_rank(&tempty[1], 0);
+    int local = 0;
+    for (int t = pair; t < items; t += n_pairs, ++local) {
+      const int buf = local & 1;
+      const uint32_t use = static_cast<uint32_t>(local >> 1);
+      const bool ok = mbar_wait_cluster(&tfull[buf], use & 1, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      int mt, nt;
+      const int z = t / tiles;
+      tile_coords(t - z * tiles, m_tiles, n_tiles, group_m, &mt, &nt);
+      epi(mt * 2 * GEMM_BM + static_cast<int>(rank) * GEMM_BM, nt * 256, z,
+          tmem_base + lane_base + buf * 256, r);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(buf ? tempty_leader1 : tempty_leader0);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 5) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+// out[i] = bf16 of the sum of `shares` fp32 partials, in share order; n8 vectors of 8
+__global__ void __launch_bounds__(256)
+    grad_reduce_kernel(const float4 *part, int shares, long n8, uint4 *out) {
+  pdl_wait();
+  pdl_trigger();
+  for (long i = blockIdx.x * static_cast<long>(blockDim.x) + threadIdx.x; i < n8;
+       i += static_cast<long>(gridDim.x) * blockDim.x) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    for (int z = 0; z < shares; ++z) {
+      const float4 p = part[(z * n8 + i) * 2], q = part[(z * n8 + i) * 2 + 1];
+      a.x += p.x; a.y += p.y; a.z += p.z; a.w += p.w;
+      b.x += q.x; b.y += q.y; b.z += q.z; b.w += q.w;
+    }
+    out[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                        pack_bf16x2(b.z, b.w));
+  }
+}
+
+}  // namespace ig4

@@ -66,6 +66,17 @@ class StackWeights(ctypes.Structure):
                 ("w_out", _vp), ("s_out", _vp), ("b_out", _vp)]
 
 
+class Rotary(ctypes.Structure):
+    _fields_ = [("B", _i), ("L", _i), ("head_dim", _i), ("rotary_dim", _i),
+                ("theta", ctypes.c_double), ("sections", _i * 3), ("interleaved", _i),
+                ("adjacent", _i), ("inverse", _i), ("dtype", _i)]
+
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", _vp), ("H", _i), ("stride_b", ctypes.c_longlong),
+                ("stride_l", ctypes.c_longlong), ("stride_h", ctypes.c_longlong)]
+
+
 def _sig(name, args, res=_i):
     fn = getattr(_lib, name)
     fn.argtypes = args
@@ -138,6 +149,16 @@ _sig("ig4_block_sp_attention", [ctypes.POINTER(Config), _i, _i, _vp, _vp, _vp, c
                                 _vp])
 _sig("ig4_block_sp_post", [ctypes.POINTER(Config), _i, _i, ctypes.POINTER(BlockWeights), _vp, _vp,
                            _vp, _vp, ctypes.c_size_t, _vp])
+_sig("ig4_add_rms_norm", [_i, _i, _vp, _vp, _i, _vp, _f, _vp, _vp, _i, _vp, _vp, _vp])
+_sig("ig4_add_rms_norm_backward_workspace_size", [_i, _i], ctypes.c_size_t)
+_sig("ig4_add_rms_norm_backward", [_i, _i, _vp, _i, _vp, _f, _vp, _i, _vp, _vp, _vp, _vp,
+                                   ctypes.c_size_t, _vp])
+_sig("ig4_mrope_rotate", [ctypes.POINTER(Rotary), _vp, ctypes.c_longlong, ctypes.POINTER(Heads),
+                          ctypes.POINTER(Heads), ctypes.POINTER(Heads), ctypes.POINTER(Heads),
+                          _vp])
+_sig("ig4_swiglu_backward_workspace_size", [_i, _i, _i], ctypes.c_size_t)
+_sig("ig4_swiglu_backward", [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
+                             _vp])
 _sig("ig4_last_device_error", [_vp])
 _sig("ig4_selftest_timeout", [_i, _vp])
 _sig("ig4_sm_clock_mhz", [_i, _vp, ctypes.POINTER(ctypes.c_double)])
@@ -156,6 +177,9 @@ EXPORTED = ("ig4_status_string", "ig4_abi_version", "ig4_mrope_positions", "ig4_
             "ig4_block_tp_attention", "ig4_block_tp_mlp", "ig4_tp_reduce", "ig4_sp_image_range",
             "ig4_sp_positions", "ig4_sp_workspace_size", "ig4_sp_exchange_bytes",
             "ig4_block_sp_pre", "ig4_block_sp_attention", "ig4_block_sp_post",
+            "ig4_add_rms_norm", "ig4_add_rms_norm_backward_workspace_size",
+            "ig4_add_rms_norm_backward", "ig4_mrope_rotate",
+            "ig4_swiglu_backward_workspace_size", "ig4_swiglu_backward",
             "ig4_last_device_error", "ig4_selftest_timeout", "ig4_sm_clock_mhz")
 
 
@@ -181,6 +205,44 @@ def _stream(stream=None):
     if torch.cuda.is_available() and torch.cuda.is_initialized():
         return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
     return ctypes.c_void_p(0)
+
+
+def _refuse(where: str):
+    raise Ig4Error(IG4_ERR_INVALID_ARG, where)
+
+
+def _same_device(where: str, *tensors) -> int:
+    """Index of the current device, on which all the given tensors (None: absent) must lie."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            _refuse(where)
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _refuse(where)
+    return dev
+
+
+def _shaped(where: str, t, shape, *dtypes):
+    """Address of a dense tensor of this shape and one of these dtypes (None stays None)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():
+        _refuse(where)
+    return t.data_ptr()
+
+
+def _workspace(where: str, workspace) -> tuple:
+    """(address, bytes) of a dense workspace tensor, or (None, 0)."""
+    if workspace is None:
+        return None, 0
+    if not workspace.is_contiguous():
+        _refuse(where)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _stream_on(dev: int, stream) -> int:
+    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
 
 
 def dtype_code(t: torch.Tensor) -> int:
@@ -488,6 +550,111 @@ def ig4_denoise_step(cfg: Config, cond: StackWeights, uncond: StackWeights, z, t
                                  _ptr(z), _ptr(text), _ptr(pos_cond), _ptr(pos_uncond),
                                  _ptr(temb_cond), _ptr(temb_uncond), t_cur, t_next, gw,
                                  _ptr(workspace), ws_bytes, _stream(stream)), "ig4_denoise_step")
+
+
+# ------------------------------------------------- operators beside the block
+# These check shapes, dtypes, density and devices of their tensors and raise
+# Ig4Error(IG4_ERR_INVALID_ARG) before the library is called.
+
+_FLOATS = (torch.float32, torch.bfloat16)
+
+
+def ig4_add_rms_norm(x, r, g, eps, s_out, y_out, y_scale_out=None, y_sf_out=None, stream=None):
+    """t = x + r; s_out = t; y_out = t rsqrt(mean(t^2) + eps) g over the last dimension.  r, g and
+    s_out may be None.  An E4M3 y_out takes y_scale_out (fp32, one per row) or y_sf_out (uint8,
+    MX8 block scales)."""
+    name = "ig4_add_rms_norm"
+    dev = _same_device(name, x, r, g, s_out, y_out, y_scale_out, y_sf_out)
+    if x.dim() < 1 or x.numel() == 0:
+        _refuse(name)
+    D = x.shape[-1]
+    M = x.numel() // D
+    if y_sf_out is not None and y_sf_out.numel() < ig4_mx8_scale_bytes(M, D):
+        _refuse(name)
+    _check(_lib.ig4_add_rms_norm(
+        M, D, _shaped(name, x, x.shape, *_FLOATS), _shaped(name, r, x.shape, x.dtype),
+        dtype_code(x), _shaped(name, g, (D,), torch.float32), eps,
+        _shaped(name, s_out, x.shape, x.dtype),
+        _shaped(name, y_out, x.shape, torch.float8_e4m3fn, *_FLOATS), dtype_code(y_out),
+        _shaped(name, y_scale_out, x.shape[:-1], torch.float32),
+        None if y_sf_out is None else _shaped(name, y_sf_out, y_sf_out.shape, torch.uint8),
+        _stream_on(dev, stream)), name)
+
+
+def ig4_add_rms_norm_backward_workspace_size(M: int, D: int) -> int:
+    return int(_lib.ig4_add_rms_norm_backward_workspace_size(M, D))
+
+
+def ig4_add_rms_norm_backward(s, g, eps, dy, ds, dx_out, dg_out, workspace=None, stream=None):
+    """Gradients of ig4_add_rms_norm: dx_out (of x and of r alike) and dg_out from dy and, unless
+    None, ds, the gradient arriving at s.  dg_out None: frozen weight (no workspace needed)."""
+    name = "ig4_add_rms_norm_backward"
+    dev = _same_device(name, s, g, dy, ds, dx_out, dg_out, workspace)
+    if s.dim() < 1 or s.numel() == 0:
+        _refuse(name)
+    D = s.shape[-1]
+    ws, ws_bytes = _workspace(name, workspace)
+    _check(_lib.ig4_add_rms_norm_backward(
+        s.numel() // D, D, _shaped(name, s, s.shape, *_FLOATS), dtype_code(s),
+        _shaped(name, g, (D,), torch.float32), eps, _shaped(name, dy, s.shape, *_FLOATS),
+        dtype_code(dy), _shaped(name, ds, s.shape, s.dtype),
+        _shaped(name, dx_out, s.shape, s.dtype), _shaped(name, dg_out, (D,), torch.float32),
+        ws, ws_bytes, _stream_on(dev, stream)), name)
+
+
+def _heads(where: str, t, like) -> Heads | None:
+    """The strided view of a [B, L, H, head_dim] tensor (elements of a head contiguous)."""
+    if t is None:
+        return None
+    B, L, H, d = t.shape if t.dim() == 4 else _refuse(where)
+    if (B, L, d) != (like.shape[0], like.shape[1], like.shape[3]) or t.dtype != like.dtype or \
+            (d > 1 and t.stride(3) != 1):
+        _refuse(where)
+    # a dimension of one element is never stepped over, whatever its stride says
+    sb, sl, sh = (st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()[:3]))
+    return Heads(t.data_ptr(), H, sb, sl, sh)
+
+
+def ig4_mrope_rotate(q, k, pos, theta, sections, q_out, k_out, rotary_dim=None, interleaved=False,
+                     adjacent=False, inverse=False, stream=None):
+    """Rotates the heads of q and (unless None) k, [B, L, H, head_dim] views of any strides, by
+    their positions pos, int32 [3, L] or [B, 3, L]; q_out / k_out may be q / k.  rotary_dim
+    defaults to twice the sum of sections; inverse=True rotates back (the gradient)."""
+    name = "ig4_mrope_rotate"
+    dev = _same_device(name, q, k, pos, q_out, k_out)
+    if q.dim() != 4 or q.dtype not in _FLOATS or pos.dtype != torch.int32 or \
+            not pos.is_contiguous() or (k is None) != (k_out is None):
+        _refuse(name)
+    B, L, _, d = q.shape
+    if tuple(pos.shape) not in ((3, L), (B, 3, L)):
+        _refuse(name)
+    rot = Rotary(B, L, d, 2 * sum(sections) if rotary_dim is None else rotary_dim, theta,
+                 (_i * 3)(*sections), int(interleaved), int(adjacent), int(inverse), dtype_code(q))
+    views = [_heads(name, t, q) for t in (q, q_out, k, k_out)]
+    _check(_lib.ig4_mrope_rotate(ctypes.byref(rot), pos.data_ptr(), 3 * L if pos.dim() == 3 else 0,
+                                 *(None if v is None else ctypes.byref(v) for v in views),
+                                 _stream_on(dev, stream)), name)
+
+
+def ig4_swiglu_backward_workspace_size(M: int, I: int, K: int) -> int:
+    return int(_lib.ig4_swiglu_backward_workspace_size(M, I, K))
+
+
+def ig4_swiglu_backward(h, w_gate, w_up, du, dh_out, dw_gate_out, dw_up_out, workspace,
+                        stream=None):
+    """Gradients of ig4_swiglu (bf16) from du: dh_out and dw_gate_out, dw_up_out (None: not
+    wanted).  h [M, K], weights [I, K], du [M, I]."""
+    name = "ig4_swiglu_backward"
+    dev = _same_device(name, h, w_gate, w_up, du, dh_out, dw_gate_out, dw_up_out, workspace)
+    if h.dim() != 2 or w_gate.dim() != 2:
+        _refuse(name)
+    (M, K), I, b = h.shape, w_gate.shape[0], torch.bfloat16
+    ws, ws_bytes = _workspace(name, workspace)
+    _check(_lib.ig4_swiglu_backward(
+        M, I, K, _shaped(name, h, (M, K), b), _shaped(name, w_gate, (I, K), b),
+        _shaped(name, w_up, (I, K), b), _shaped(name, du, (M, I), b),
+        _shaped(name, dh_out, (M, K), b), _shaped(name, dw_gate_out, (I, K), b),
+        _shaped(name, dw_up_out, (I, K), b), ws, ws_bytes, _stream_on(dev, stream)), name)
 
 
 def ig4_last_device_error(stream=None) -> int:
