@@ -327,6 +327,26 @@ ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long
                             const ig4_heads *q, const ig4_heads *q_out, const ig4_heads *k,
                             const ig4_heads *k_out, void *stream);
 
+/* -------------------------------------------- few rows x NVFP4 weights ---
+ * ig4_nvfp4_linear's weights for 1 to 8 rows (single tokens of up to 8
+ * sequences) with bf16 activations: no activation is quantised,
+ *   out[m][n] = w_scale[n] * sum_k x[m][k] W(n,k) (+ bias[n]),
+ *   W(n,k) = e4m3(w_sf[n][k/16]) * e2m1(w_code[n][k]),
+ * products exact (x down to 2^-28 of its largest neighbours), sums fp32.  x bf16
+ * [M][K]; w_codes [N][K/2]; w_sf packed by ig4_nvfp4_pack_scales; w_scale [N],
+ * bias [N] (or NULL) fp32; out [M][N] fp32 or bf16 (out_dtype).
+ * ig4_nvfp4_swiglu_matvec: the gated pair, u_out[m][i] = silu(g) * up bf16 [M][I]
+ * with g and up the two products.  1 <= M <= 8, N, I >= 1 (any), K % 64 == 0,
+ * K <= 24576; x, codes and scales 16-byte aligned; the output overlaps no
+ * input.  Errors: INVALID_ARG. */
+ig4_status ig4_nvfp4_matvec(int M, int N, int K, const void *x, const void *w_codes,
+                            const void *w_sf, const float *w_scale, const float *bias, void *out,
+                            int out_dtype, void *stream);
+ig4_status ig4_nvfp4_swiglu_matvec(int M, int I, int K, const void *x, const void *gate_codes,
+                                   const void *gate_sf, const float *gate_scale,
+                                   const void *up_codes, const void *up_sf,
+                                   const float *up_scale, void *u_out, void *stream);
+
 /* ------------------------------------------------------ SwiGLU gradients ---
  * Gradients of ig4_swiglu's u = silu(G) * U, G = h W_gate^T, U = h W_up^T (bf16
  * weights), from du = dL/du:

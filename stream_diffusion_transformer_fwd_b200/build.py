@@ -22,7 +22,7 @@ SOURCES = ["ig4_api.cu"]
 DEPS = ["ig4_api.cu", "ig4_ptx.cuh", "ig4_gemm.cuh", "ig4_attention.cuh", "ig4_small.cuh",
         "ig4_mx8.cuh",
         "ig4_nvf4.cuh", "ig4_parallel.cuh", "ig4_addnorm.cuh", "ig4_rotate.cuh",
-        "ig4_ffn_grad.cuh"]
+        "ig4_ffn_grad.cuh", "ig4_matvec.cuh"]
 
 
 def nvcc_path() -> str:

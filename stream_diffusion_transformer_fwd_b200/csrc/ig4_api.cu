@@ -19,6 +19,7 @@
 #include "ig4_attention.cuh"
 #include "ig4_ffn_grad.cuh"
 #include "ig4_gemm.cuh"
+#include "ig4_matvec.cuh"
 #include "ig4_mx8.cuh"
 #include "ig4_nvf4.cuh"
 #include "ig4_parallel.cuh"
@@ -2554,6 +2555,74 @@ ig4_status launch_rotate_v(const RotateArgs &a, bool adjacent, dim3 grid, cudaSt
   return e == cudaSuccess ? last_launch_status() : IG4_ERR_CUDA;
 }
 
+// ---- few rows x NVFP4 weights
+
+template <int C, bool DUAL, typename OT>
+ig4_status launch_matvec_c(int M, int N, int K, const void *x, const MatvecWeights &w0,
+                           const MatvecWeights &w1, const float *bias, void *out, int cluster,
+                           cudaStream_t st) {
+  DeviceInfo *di = nullptr;
+  IG4_TRY(device_info(&di));
+  const int tiles = (N + 127) / 128 * 8;
+  const int clusters = std::min(tiles, std::max(1, 2 * di->sms / cluster));
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(clusters * cluster);
+  lc.blockDim = dim3(MATVEC_THREADS);
+  lc.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = cluster > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&lc, nvfp4_matvec_kernel<C, DUAL, OT>,
+                         static_cast<const __nv_bfloat16 *>(x), w0, w1, bias,
+                         static_cast<OT *>(out), M, N, K, tiles, cluster) != cudaSuccess)
+    return IG4_ERR_CUDA;
+  return last_launch_status();
+}
+
+// Cluster size: the smallest that brings a warp's share of K down to
+// MATVEC_MAX_CHUNKS chunks, doubled while row tiles leave SMs without a CTA and
+// every warp still has a chunk.
+template <bool DUAL, typename OT>
+ig4_status launch_matvec(int M, int N, int K, const void *x, const MatvecWeights &w0,
+                         const MatvecWeights &w1, const float *bias, void *out, cudaStream_t st) {
+  const int nc = (K + MATVEC_CHUNK - 1) / MATVEC_CHUNK;
+  const long tiles = (N + 127L) / 128 * 8;
+  auto chunks = [&](int cl) { return (nc + cl * MATVEC_WARPS - 1) / (cl * MATVEC_WARPS); };
+  int cl = 1;
+  while (chunks(cl) > MATVEC_MAX_CHUNKS) cl *= 2;
+  while (cl < MATVEC_MAX_CLUSTER && tiles * cl < 148 && nc >= 2 * cl * MATVEC_WARPS) cl *= 2;
+  switch (chunks(cl)) {
+    case 1: return launch_matvec_c<1, DUAL, OT>(M, N, K, x, w0, w1, bias, out, cl, st);
+    case 2: return launch_matvec_c<2, DUAL, OT>(M, N, K, x, w0, w1, bias, out, cl, st);
+    default: return launch_matvec_c<3, DUAL, OT>(M, N, K, x, w0, w1, bias, out, cl, st);
+  }
+}
+
+bool matvec_args_ok(int M, int N, int K, const void *x, const MatvecWeights *w, int n_w,
+                    const float *bias, const void *out, size_t out_esize) {
+  if (M < 1 || M > 8 || N < 1 || N > (1 << 26) || K < 64 || K % 64 ||
+      K > MATVEC_MAX_CLUSTER * MATVEC_WARPS * MATVEC_MAX_CHUNKS * MATVEC_CHUNK || !x || !out ||
+      !aligned16(x) || reinterpret_cast<uintptr_t>(out) % out_esize ||
+      reinterpret_cast<uintptr_t>(bias) % 4)
+    return false;
+  const size_t n = N;
+  const Span o{out, n * M * out_esize};
+  if (overlap(o, {x, static_cast<size_t>(M) * K * 2}) || overlap(o, {bias, n * 4})) return false;
+  for (int i = 0; i < n_w; ++i) {
+    if (!w[i].codes || !w[i].sf || !w[i].scale || !aligned16(w[i].codes) || !aligned16(w[i].sf) ||
+        reinterpret_cast<uintptr_t>(w[i].scale) % 4 || overlap(o, {w[i].codes, n * (K / 2)}) ||
+        overlap(o, {w[i].sf, (n + 127) / 128 * 128 * (K / 16)}) || overlap(o, {w[i].scale, n * 4}))
+      return false;
+  }
+  return true;
+}
+
 // ---- SwiGLU gradients
 
 // MN-major operand (see ig4_ffn_grad.cuh): bf16 matrix [rows][cols], rows the
@@ -2786,6 +2855,32 @@ ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long
                  : launch_rotate_v<float, 1>(a, adj, grid, st);
   return V > 1 ? launch_rotate_v<__nv_bfloat16, 8>(a, adj, grid, st)
                : launch_rotate_v<__nv_bfloat16, 1>(a, adj, grid, st);
+}
+
+ig4_status ig4_nvfp4_matvec(int M, int N, int K, const void *x, const void *w_codes,
+                            const void *w_sf, const float *w_scale, const float *bias, void *out,
+                            int out_dtype, void *stream) {
+  const MatvecWeights w{static_cast<const uint8_t *>(w_codes), static_cast<const uint8_t *>(w_sf),
+                        w_scale};
+  if (!valid_dtype_x(out_dtype) ||
+      !matvec_args_ok(M, N, K, x, &w, 1, bias, out, esize_of(out_dtype)))
+    return IG4_ERR_INVALID_ARG;
+  return out_dtype == IG4_F32
+             ? launch_matvec<false, float>(M, N, K, x, w, w, bias, out, as_stream(stream))
+             : launch_matvec<false, __nv_bfloat16>(M, N, K, x, w, w, bias, out, as_stream(stream));
+}
+
+ig4_status ig4_nvfp4_swiglu_matvec(int M, int I, int K, const void *x, const void *gate_codes,
+                                   const void *gate_sf, const float *gate_scale,
+                                   const void *up_codes, const void *up_sf,
+                                   const float *up_scale, void *u_out, void *stream) {
+  const MatvecWeights w[2] = {{static_cast<const uint8_t *>(gate_codes),
+                               static_cast<const uint8_t *>(gate_sf), gate_scale},
+                              {static_cast<const uint8_t *>(up_codes),
+                               static_cast<const uint8_t *>(up_sf), up_scale}};
+  if (!matvec_args_ok(M, I, K, x, w, 2, nullptr, u_out, 2)) return IG4_ERR_INVALID_ARG;
+  return launch_matvec<true, __nv_bfloat16>(M, I, K, x, w[0], w[1], nullptr, u_out,
+                                            as_stream(stream));
 }
 
 size_t ig4_swiglu_backward_workspace_size(int M, int I, int K) {

@@ -156,6 +156,8 @@ _sig("ig4_add_rms_norm_backward", [_i, _i, _vp, _i, _vp, _f, _vp, _i, _vp, _vp, 
 _sig("ig4_mrope_rotate", [ctypes.POINTER(Rotary), _vp, ctypes.c_longlong, ctypes.POINTER(Heads),
                           ctypes.POINTER(Heads), ctypes.POINTER(Heads), ctypes.POINTER(Heads),
                           _vp])
+_sig("ig4_nvfp4_matvec", [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp])
+_sig("ig4_nvfp4_swiglu_matvec", [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp])
 _sig("ig4_swiglu_backward_workspace_size", [_i, _i, _i], ctypes.c_size_t)
 _sig("ig4_swiglu_backward", [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
                              _vp])
@@ -178,7 +180,8 @@ EXPORTED = ("ig4_status_string", "ig4_abi_version", "ig4_mrope_positions", "ig4_
             "ig4_sp_positions", "ig4_sp_workspace_size", "ig4_sp_exchange_bytes",
             "ig4_block_sp_pre", "ig4_block_sp_attention", "ig4_block_sp_post",
             "ig4_add_rms_norm", "ig4_add_rms_norm_backward_workspace_size",
-            "ig4_add_rms_norm_backward", "ig4_mrope_rotate",
+            "ig4_add_rms_norm_backward", "ig4_mrope_rotate", "ig4_nvfp4_matvec",
+            "ig4_nvfp4_swiglu_matvec",
             "ig4_swiglu_backward_workspace_size", "ig4_swiglu_backward",
             "ig4_last_device_error", "ig4_selftest_timeout", "ig4_sm_clock_mhz")
 
@@ -634,6 +637,43 @@ def ig4_mrope_rotate(q, k, pos, theta, sections, q_out, k_out, rotary_dim=None, 
     _check(_lib.ig4_mrope_rotate(ctypes.byref(rot), pos.data_ptr(), 3 * L if pos.dim() == 3 else 0,
                                  *(None if v is None else ctypes.byref(v) for v in views),
                                  _stream_on(dev, stream)), name)
+
+
+def _nvfp4(where: str, codes, sf, scale, K: int) -> tuple:
+    """Addresses of NVFP4 weights [N, K]: codes uint8 [N, K/2], packed scales, fp32 scale [N]."""
+    N = codes.shape[0]
+    if sf.numel() < ig4_nvfp4_scale_bytes(N, K):
+        _refuse(where)
+    return (_shaped(where, codes, (N, K // 2), torch.uint8),
+            _shaped(where, sf, sf.shape, torch.uint8), _shaped(where, scale, (N,), torch.float32))
+
+
+def ig4_nvfp4_matvec(x, w_codes, w_sf, w_scale, bias, out, stream=None):
+    """out [M, N] (fp32 or bf16) = x [M, K] (bf16, M <= 8) times NVFP4 weights (+ bias)."""
+    name = "ig4_nvfp4_matvec"
+    dev = _same_device(name, x, w_codes, w_sf, w_scale, bias, out)
+    if x.dim() != 2 or w_codes.dim() != 2:
+        _refuse(name)
+    (M, K), N = x.shape, w_codes.shape[0]
+    _check(_lib.ig4_nvfp4_matvec(
+        M, N, K, _shaped(name, x, (M, K), torch.bfloat16), *_nvfp4(name, w_codes, w_sf, w_scale, K),
+        _shaped(name, bias, (N,), torch.float32), _shaped(name, out, (M, N), *_FLOATS),
+        dtype_code(out), _stream_on(dev, stream)), name)
+
+
+def ig4_nvfp4_swiglu_matvec(x, gate_codes, gate_sf, gate_scale, up_codes, up_sf, up_scale, u_out,
+                            stream=None):
+    """u_out [M, I] bf16 = silu(x Wg^T) * (x Wu^T), x [M, K] bf16, M <= 8, NVFP4 weights."""
+    name = "ig4_nvfp4_swiglu_matvec"
+    dev = _same_device(name, x, gate_codes, gate_sf, gate_scale, up_codes, up_sf, up_scale, u_out)
+    if x.dim() != 2 or gate_codes.dim() != 2 or up_codes.shape != gate_codes.shape:
+        _refuse(name)
+    (M, K), I = x.shape, gate_codes.shape[0]
+    _check(_lib.ig4_nvfp4_swiglu_matvec(
+        M, I, K, _shaped(name, x, (M, K), torch.bfloat16),
+        *_nvfp4(name, gate_codes, gate_sf, gate_scale, K),
+        *_nvfp4(name, up_codes, up_sf, up_scale, K), _shaped(name, u_out, (M, I), torch.bfloat16),
+        _stream_on(dev, stream)), name)
 
 
 def ig4_swiglu_backward_workspace_size(M: int, I: int, K: int) -> int:

@@ -156,6 +156,36 @@ def test_swiglu_backward_sizes_and_workspace(ig4):
         assert ig4.ig4_swiglu_backward_workspace_size(*sizes) == 0
 
 
+# ------------------------------------------------------ few rows x NVFP4 weights
+
+def matvec(ig4, M=2, N=256, K=128, x=at(0), c=at(1), sf=at(2), sc=at(3), b=at(4), out=at(5),
+           od=BF16):
+    return ig4.library().ig4_nvfp4_matvec(M, N, K, x, c, sf, sc, b, out, od, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(M=0), dict(M=9), dict(N=0), dict(K=0), dict(K=96), dict(K=24640), dict(x=None),
+    dict(c=None), dict(sf=None), dict(sc=None), dict(out=None), dict(od=E4M3), dict(x=at(0, 8)),
+    dict(c=at(1, 8)), dict(sf=at(2, 8)), dict(sc=at(3, 2)), dict(b=at(4, 2)), dict(out=at(5, 1)),
+    dict(out=at(5, 2), od=F32), dict(out=at(0)), dict(out=at(1, 64)), dict(out=at(2)),
+    dict(out=at(3)), dict(out=at(4))])
+def test_nvfp4_matvec_refuses(ig4, bad):
+    assert matvec(ig4, **bad) == ig4.IG4_ERR_INVALID_ARG
+
+
+def gated(ig4, M=2, I=256, K=128, x=at(0), gc=at(1), gs=at(2), gf=at(3), uc=at(4), us=at(5),
+          uf=at(6), out=at(7)):
+    return ig4.library().ig4_nvfp4_swiglu_matvec(M, I, K, x, gc, gs, gf, uc, us, uf, out, None)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(M=0), dict(M=9), dict(I=0), dict(K=32), dict(x=None), dict(gc=None), dict(gs=None),
+    dict(gf=None), dict(uc=None), dict(us=None), dict(uf=None), dict(out=None), dict(uc=at(4, 8)),
+    dict(us=at(5, 8)), dict(uf=at(6, 2)), dict(out=at(7, 1)), dict(out=at(4)), dict(out=at(6))])
+def test_nvfp4_swiglu_matvec_refuses(ig4, bad):
+    assert gated(ig4, **bad) == ig4.IG4_ERR_INVALID_ARG
+
+
 # ------------------------------------------------------------------- binding
 
 def test_binding_refuses_host_tensors(ig4):
