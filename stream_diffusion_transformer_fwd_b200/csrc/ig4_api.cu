@@ -8,6 +8,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -91,6 +92,9 @@ ig4_status last_launch_status() {
 // Per-device facts queried once.
 struct DeviceInfo {
   int sms = 0;
+  // clusters of 2, 4, 8 CTAs of the matvec kernels that run at once, with 1 to 3
+  // CTAs on an SM ([gated][fp32 output][size][CTAs]; 0: not asked yet)
+  std::atomic<int> clusters[2][2][3][3] = {};
 };
 constexpr int MAX_DEVICES = 64;
 DeviceInfo g_dev[MAX_DEVICES];
@@ -2441,24 +2445,34 @@ inline size_t esize_of(int dt) { return dt == IG4_F32 ? 4 : (dt == IG4_BF16 ? 2 
 bool addnorm_sizes_ok(int M, int D) { return M >= 1 && D >= 8 && D % 8 == 0 && D <= 8192; }
 
 // Launch shape: a warp per row up to ADDNORM_WARP_D, else a CTA of as many
-// warps as cover the row with ADDNORM_NV vectors per thread; `per_sm` CTAs on
-// each SM walk the rows.
+// warps as cover the row with ADDNORM_NV vectors per thread, `ctas` of them on
+// an SM, walking the rows.  The ring gets the SM's shared memory in equal
+// parts, at least two slots (a row's inputs) per CTA.
 struct AddNormPlan {
   bool warp;
-  int threads, grid;
+  int threads, grid, slots;
+  size_t smem;
 };
-AddNormPlan addnorm_plan(int M, int D, int sms, int threads_per_sm) {
+constexpr size_t ADDNORM_SM_SMEM = 220 << 10;
+AddNormPlan addnorm_plan(int M, int D, size_t slot_bytes, int sms, int threads_per_sm) {
   AddNormPlan p{};
   p.warp = D <= ADDNORM_WARP_D;
   const int nvec = D / 8;
   p.threads = p.warp ? 32 * ADDNORM_WARPS : 32 * ((nvec + 32 * ADDNORM_NV - 1) / (32 * ADDNORM_NV));
+  int ctas = std::max(1, std::min(threads_per_sm, p.warp ? 512 : 2048) / p.threads);
+  if (!p.warp) {
+    while (ctas > 1 && ctas * (addnorm_smem(slot_bytes, 2) + 1024) > ADDNORM_SM_SMEM) --ctas;
+    p.slots = 2;
+    while (p.slots < ADDNORM_MAX_SLOTS &&
+           ctas * (addnorm_smem(slot_bytes, p.slots + 1) + 1024) <= ADDNORM_SM_SMEM)
+      ++p.slots;
+  }
   const long rows = p.warp ? (M + ADDNORM_WARPS - 1L) / ADDNORM_WARPS : M;
-  const int per_sm = std::max(1, threads_per_sm / p.threads);
-  p.grid = static_cast<int>(std::min<long>(rows, static_cast<long>(sms) * per_sm));
+  p.grid = static_cast<int>(std::min<long>(rows, static_cast<long>(sms) * ctas));
+  p.slots = static_cast<int>(std::min<long>(p.slots, (rows + p.grid - 1) / p.grid));
+  p.smem = addnorm_smem(slot_bytes, p.slots);
   return p;
 }
-constexpr int ADDNORM_FWD_THREADS_PER_SM = 1024;
-constexpr int ADDNORM_BWD_THREADS_PER_SM = 576;
 constexpr int ADDNORM_MAX_SMS = 160;  // bounds the partial rows of dg in the workspace
 
 template <typename XT, int OUT>
@@ -2466,15 +2480,20 @@ ig4_status launch_add_norm_t(int M, int D, const void *x, const void *r, const f
                              void *s, void *y, float *scale, void *sf, cudaStream_t st) {
   DeviceInfo *di = nullptr;
   IG4_TRY(device_info(&di));
-  const AddNormPlan p = addnorm_plan(M, D, di->sms, ADDNORM_FWD_THREADS_PER_SM);
+  const AddNormPlan p = addnorm_plan(M, D, (r ? 2 : 1) * sizeof(XT) * D, di->sms,
+                                     ADDNORM_FWD_THREADS_PER_SM);
   const XT *xp = static_cast<const XT *>(x), *rp = static_cast<const XT *>(r);
   XT *sp = static_cast<XT *>(s);
   uint8_t *sfp = static_cast<uint8_t *>(sf);
-  const cudaError_t e =
-      p.warp ? launch_pdl(add_rms_norm_kernel<XT, OUT, ADDNORM_NV, true>, dim3(p.grid),
-                          dim3(p.threads), 0, st, xp, rp, g, eps, sp, y, scale, sfp, M, D)
-             : launch_pdl(add_rms_norm_kernel<XT, OUT, ADDNORM_NV, false>, dim3(p.grid),
-                          dim3(p.threads), 0, st, xp, rp, g, eps, sp, y, scale, sfp, M, D);
+  cudaError_t e;
+  if (p.warp) {
+    e = launch_pdl(add_rms_norm_warp_kernel<XT, OUT>, dim3(p.grid), dim3(p.threads), 0, st, xp, rp,
+                   g, eps, sp, y, scale, sfp, M, D);
+  } else {
+    IG4_TRY(allow_smem(add_rms_norm_kernel<XT, OUT>, static_cast<int>(p.smem)));
+    e = launch_pdl(add_rms_norm_kernel<XT, OUT>, dim3(p.grid), dim3(p.threads), p.smem, st, xp, rp,
+                   g, eps, sp, y, scale, sfp, M, D, p.slots);
+  }
   return e == cudaSuccess ? last_launch_status() : IG4_ERR_CUDA;
 }
 
@@ -2499,21 +2518,26 @@ ig4_status launch_add_norm_grad(int M, int D, const void *s, const float *g, flo
                                 cudaStream_t st) {
   DeviceInfo *di = nullptr;
   IG4_TRY(device_info(&di));
-  const AddNormPlan p =
-      addnorm_plan(M, D, std::min(di->sms, ADDNORM_MAX_SMS), ADDNORM_BWD_THREADS_PER_SM);
+  const size_t slot = static_cast<size_t>(D) * ((ds ? 2 : 1) * sizeof(XT) + sizeof(YT));
+  const AddNormPlan p = addnorm_plan(M, D, slot, std::min(di->sms, ADDNORM_MAX_SMS),
+                                     ADDNORM_BWD_THREADS_PER_SM);
   float *pp = dg ? part : nullptr;
   const XT *sp = static_cast<const XT *>(s), *dsp = static_cast<const XT *>(ds);
   const YT *dyp = static_cast<const YT *>(dy);
   XT *dxp = static_cast<XT *>(dx);
-  const cudaError_t e =
-      p.warp ? launch_pdl(add_rms_norm_grad_kernel<XT, YT, ADDNORM_NV, true>, dim3(p.grid),
-                          dim3(p.threads), 0, st, sp, g, eps, dyp, dsp, dxp, pp, M, D)
-             : launch_pdl(add_rms_norm_grad_kernel<XT, YT, ADDNORM_NV, false>, dim3(p.grid),
-                          dim3(p.threads), 0, st, sp, g, eps, dyp, dsp, dxp, pp, M, D);
+  cudaError_t e;
+  if (p.warp) {
+    e = launch_pdl(add_rms_norm_grad_warp_kernel<XT, YT>, dim3(p.grid), dim3(p.threads), 0, st, sp,
+                   g, eps, dyp, dsp, dxp, pp, M, D);
+  } else {
+    IG4_TRY(allow_smem(add_rms_norm_grad_kernel<XT, YT>, static_cast<int>(p.smem)));
+    e = launch_pdl(add_rms_norm_grad_kernel<XT, YT>, dim3(p.grid), dim3(p.threads), p.smem, st, sp,
+                   g, eps, dyp, dsp, dxp, pp, M, D, p.slots);
+  }
   if (e != cudaSuccess) return IG4_ERR_CUDA;
   IG4_TRY(last_launch_status());
   if (!dg) return IG4_OK;
-  if (launch_pdl(add_rms_norm_dg_kernel, dim3((D + 31) / 32), dim3(ADDNORM_DG_THREADS), 0, st,
+  if (launch_pdl(add_rms_norm_dg_kernel, dim3(D / ADDNORM_DG_COLS), dim3(ADDNORM_DG_THREADS), 0, st,
                  static_cast<const float *>(part), p.grid, D, dg) != cudaSuccess)
     return IG4_ERR_CUDA;
   return last_launch_status();
@@ -2547,6 +2571,25 @@ bool heads_vec(const ig4_heads &t, int V, int esize) {
          t.stride_l % V == 0 && t.stride_h % V == 0;
 }
 
+// Threads of a walk over U units and up to nh heads: the head group HG (with
+// as many tokens side by side as then fit, at most max_tg) that leaves the
+// fewest threads and head steps idle.
+RotateWalk rotate_walk_plan(int U, int nh, int max_tg) {
+  RotateWalk k{};
+  if (U <= 0) return k;
+  double best = 0.0;
+  for (int hg = 1; hg <= nh && hg * U <= ROTATE_THREADS; ++hg) {
+    const int tg = std::min(max_tg, ROTATE_THREADS / (U * hg));
+    const int steps = (nh + hg - 1) / hg;
+    const double used = static_cast<double>(U) * tg * nh / steps;
+    if (used > best) {
+      best = used;
+      k = {U, hg, tg, (65536 + U - 1) / U, (65536 + hg - 1) / hg};
+    }
+  }
+  return k;
+}
+
 template <typename T, int V>
 ig4_status launch_rotate_v(const RotateArgs &a, bool adjacent, dim3 grid, cudaStream_t st) {
   const cudaError_t e =
@@ -2557,17 +2600,28 @@ ig4_status launch_rotate_v(const RotateArgs &a, bool adjacent, dim3 grid, cudaSt
 
 // ---- few rows x NVFP4 weights
 
-template <int C, bool DUAL, typename OT>
-ig4_status launch_matvec_c(int M, int N, int K, const void *x, const MatvecWeights &w0,
-                           const MatvecWeights &w1, const float *bias, void *out, int cluster,
-                           cudaStream_t st) {
+// Cluster size: the smallest that brings a CTA's share of x under
+// MATVEC_MAX_X_BYTES (then three CTAs, or two, fit an SM), doubled while row
+// tiles leave SMs without a CTA and every warp still has two chunks.
+template <bool DUAL, typename OT>
+ig4_status launch_matvec(int M, int N, int K, const void *x, const MatvecWeights &w0,
+                         const MatvecWeights &w1, const float *bias, void *out, cudaStream_t st) {
   DeviceInfo *di = nullptr;
   IG4_TRY(device_info(&di));
+  const int nc = (K + MATVEC_CHUNK - 1) / MATVEC_CHUNK;
   const int tiles = (N + 127) / 128 * 8;
-  const int clusters = std::min(tiles, std::max(1, 2 * di->sms / cluster));
+  int cluster = 1;
+  auto x_bytes = [&] { return matvec_x_bytes((nc + cluster - 1) / cluster, M); };
+  while (cluster < MATVEC_MAX_CLUSTER && x_bytes() > MATVEC_MAX_X_BYTES) cluster *= 2;
+  while (cluster < MATVEC_MAX_CLUSTER && static_cast<long>(tiles) * cluster < di->sms &&
+         nc >= 4 * cluster * MATVEC_WARPS)
+    cluster *= 2;
+  const int smem = MATVEC_RING_BYTES + x_bytes();
+  auto kern = nvfp4_matvec_kernel<DUAL, OT>;
+  IG4_TRY(allow_smem(kern, smem));
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(clusters * cluster);
   lc.blockDim = dim3(MATVEC_THREADS);
+  lc.dynamicSmemBytes = smem;
   lc.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -2578,36 +2632,33 @@ ig4_status launch_matvec_c(int M, int N, int K, const void *x, const MatvecWeigh
   attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = cluster > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&lc, nvfp4_matvec_kernel<C, DUAL, OT>,
-                         static_cast<const __nv_bfloat16 *>(x), w0, w1, bias,
+  // Row tiles are dealt out in advance, so all CTAs have to run at once.  With
+  // clusters the device holds fewer than its SMs suggest (a cluster stays in one
+  // GPC); how many, for so many CTAs on an SM, is asked once.
+  const int per_sm = std::min(MATVEC_CTAS, MATVEC_SM_SMEM / (smem + MATVEC_STATIC_SMEM));
+  int most = per_sm * di->sms;
+  if (cluster > 1) {
+    const int lg = cluster == 2 ? 0 : cluster == 4 ? 1 : 2;
+    std::atomic<int> &known = di->clusters[DUAL ? 1 : 0][sizeof(OT) == 4][lg][per_sm - 1];
+    most = known.load(std::memory_order_relaxed);
+    if (most == 0) {
+      lc.gridDim = dim3(di->sms / cluster * cluster);
+      if (cudaOccupancyMaxActiveClusters(&most, kern, &lc) != cudaSuccess || most < 1)
+        return IG4_ERR_CUDA;
+      known.store(most, std::memory_order_relaxed);
+    }
+  }
+  lc.gridDim = dim3(std::min(tiles, most) * cluster);
+  if (cudaLaunchKernelEx(&lc, kern, static_cast<const __nv_bfloat16 *>(x), w0, w1, bias,
                          static_cast<OT *>(out), M, N, K, tiles, cluster) != cudaSuccess)
     return IG4_ERR_CUDA;
   return last_launch_status();
 }
 
-// Cluster size: the smallest that brings a warp's share of K down to
-// MATVEC_MAX_CHUNKS chunks, doubled while row tiles leave SMs without a CTA and
-// every warp still has a chunk.
-template <bool DUAL, typename OT>
-ig4_status launch_matvec(int M, int N, int K, const void *x, const MatvecWeights &w0,
-                         const MatvecWeights &w1, const float *bias, void *out, cudaStream_t st) {
-  const int nc = (K + MATVEC_CHUNK - 1) / MATVEC_CHUNK;
-  const long tiles = (N + 127L) / 128 * 8;
-  auto chunks = [&](int cl) { return (nc + cl * MATVEC_WARPS - 1) / (cl * MATVEC_WARPS); };
-  int cl = 1;
-  while (chunks(cl) > MATVEC_MAX_CHUNKS) cl *= 2;
-  while (cl < MATVEC_MAX_CLUSTER && tiles * cl < 148 && nc >= 2 * cl * MATVEC_WARPS) cl *= 2;
-  switch (chunks(cl)) {
-    case 1: return launch_matvec_c<1, DUAL, OT>(M, N, K, x, w0, w1, bias, out, cl, st);
-    case 2: return launch_matvec_c<2, DUAL, OT>(M, N, K, x, w0, w1, bias, out, cl, st);
-    default: return launch_matvec_c<3, DUAL, OT>(M, N, K, x, w0, w1, bias, out, cl, st);
-  }
-}
-
 bool matvec_args_ok(int M, int N, int K, const void *x, const MatvecWeights *w, int n_w,
                     const float *bias, const void *out, size_t out_esize) {
   if (M < 1 || M > 8 || N < 1 || N > (1 << 26) || K < 64 || K % 64 ||
-      K > MATVEC_MAX_CLUSTER * MATVEC_WARPS * MATVEC_MAX_CHUNKS * MATVEC_CHUNK || !x || !out ||
+      K > MATVEC_MAX_K || !x || !out ||
       !aligned16(x) || reinterpret_cast<uintptr_t>(out) % out_esize ||
       reinterpret_cast<uintptr_t>(bias) % 4)
     return false;
@@ -2750,7 +2801,8 @@ ig4_status ig4_add_rms_norm(int M, int D, const void *x, const void *r, int x_dt
 
 size_t ig4_add_rms_norm_backward_workspace_size(int M, int D) {
   if (!addnorm_sizes_ok(M, D)) return 0;
-  const AddNormPlan p = addnorm_plan(M, D, ADDNORM_MAX_SMS, ADDNORM_BWD_THREADS_PER_SM);
+  // the smallest slots allow the most CTAs
+  const AddNormPlan p = addnorm_plan(M, D, 4ul * D, ADDNORM_MAX_SMS, ADDNORM_BWD_THREADS_PER_SM);
   return round_up(static_cast<size_t>(p.grid) * D * 4, 256);
 }
 
@@ -2804,10 +2856,11 @@ ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long
   const int es = static_cast<int>(esize_of(rot->dtype));
   RotateArgs a{};
   const ig4_heads *ins[2] = {q, k}, *outs[2] = {q_out, k_out};
-  int V = 16 / es;
-  // whole vectors in both halves of a head and past the rotary elements
+  // the widest vectors that fit both halves of a head, the elements past them,
+  // and every address
   const int half = rot->adjacent ? R : R / 2;
-  if (half % V || (d - R) % V) V = 1;
+  int V = 16 / es;
+  while (half % V || (d - R) % V) V /= 2;
   int heads = 0;
   for (int w = 0; w < 2; ++w) {
     if (!ins[w]) continue;
@@ -2817,9 +2870,9 @@ ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long
     if (i.data == o.data &&
         (i.stride_b != o.stride_b || i.stride_l != o.stride_l || i.stride_h != o.stride_h))
       return IG4_ERR_INVALID_ARG;
-    if (!heads_vec(i, V, es) || !heads_vec(o, V, es)) V = 1;
+    while (!heads_vec(i, V, es) || !heads_vec(o, V, es)) V /= 2;
     a.t[w] = {i.data, o.data, i.H, i.stride_b, i.stride_l, i.stride_h,
-              o.stride_b, o.stride_l, o.stride_h};
+              o.stride_b, o.stride_l, o.stride_h, {}, {}};
     heads += i.H;
   }
   if (k_out && k_out->data == q_out->data) return IG4_ERR_INVALID_ARG;
@@ -2840,21 +2893,37 @@ ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long
   a.R = R;
   a.log2_theta = std::log2(rot->theta);
   a.sin_sign = rot->inverse ? -1.0f : 1.0f;
-  // Tokens per CTA: as many as keep 4 CTAs for every SM, up to 4 and to the
-  // table's size; with fewer tokens than that the heads are shared out too.
-  const long ntok = static_cast<long>(B) * L, want = 4L * di->sms;
-  a.tt = static_cast<int>(std::max<long>(
-      1, std::min<long>({4, ROTATE_TABLE / (R / 2), ntok / want})));
+  // Tokens per CTA: one wave of CTAs (ROTATE_CTAS fit on an SM) as long as the
+  // table holds that many; with fewer tokens than a wave has CTAs the heads are
+  // shared out too.
+  const long ntok = static_cast<long>(B) * L, want = static_cast<long>(ROTATE_CTAS) * di->sms;
+  a.tt = static_cast<int>(
+      std::min<long>({ROTATE_MAX_TOKENS, ROTATE_TABLE / (R / 2), (ntok + want - 1) / want}));
   const long tiles = (ntok + a.tt - 1) / a.tt;
   a.hs = static_cast<int>(std::max<long>(1, std::min<long>({heads, 64, want / tiles})));
+  const int units = rot->adjacent ? (V >= 2 ? R / V : R / 2) : R / 2 / V;
+  for (RotateHeads &t : a.t) {
+    const int nh = (t.H + a.hs - 1) / a.hs;
+    t.turn = rotate_walk_plan(t.H ? units : 0, nh, a.tt);
+    // the elements past the rotary ones: walks over equal runs of at most 256
+    // vectors (none in place)
+    const int vecs = t.H && t.in != t.out ? (d - R) / V : 0;
+    int runs = 1;
+    while (vecs / runs > ROTATE_THREADS || vecs % runs) ++runs;
+    t.copy = rotate_walk_plan(vecs / runs, nh, a.tt);
+  }
   const dim3 grid(static_cast<unsigned>(tiles), a.hs);
   cudaStream_t st = as_stream(stream);
   const bool adj = rot->adjacent != 0;
-  if (rot->dtype == IG4_F32)
-    return V > 1 ? launch_rotate_v<float, 4>(a, adj, grid, st)
-                 : launch_rotate_v<float, 1>(a, adj, grid, st);
-  return V > 1 ? launch_rotate_v<__nv_bfloat16, 8>(a, adj, grid, st)
-               : launch_rotate_v<__nv_bfloat16, 1>(a, adj, grid, st);
+  if (rot->dtype == IG4_F32) {
+    if (V == 4) return launch_rotate_v<float, 4>(a, adj, grid, st);
+    if (V == 2) return launch_rotate_v<float, 2>(a, adj, grid, st);
+    return launch_rotate_v<float, 1>(a, adj, grid, st);
+  }
+  if (V == 8) return launch_rotate_v<__nv_bfloat16, 8>(a, adj, grid, st);
+  if (V == 4) return launch_rotate_v<__nv_bfloat16, 4>(a, adj, grid, st);
+  if (V == 2) return launch_rotate_v<__nv_bfloat16, 2>(a, adj, grid, st);
+  return launch_rotate_v<__nv_bfloat16, 1>(a, adj, grid, st);
 }
 
 ig4_status ig4_nvfp4_matvec(int M, int N, int K, const void *x, const void *w_codes,

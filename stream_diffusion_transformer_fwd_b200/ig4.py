@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -153,9 +154,7 @@ _sig("ig4_add_rms_norm", [_i, _i, _vp, _vp, _i, _vp, _f, _vp, _vp, _i, _vp, _vp,
 _sig("ig4_add_rms_norm_backward_workspace_size", [_i, _i], ctypes.c_size_t)
 _sig("ig4_add_rms_norm_backward", [_i, _i, _vp, _i, _vp, _f, _vp, _i, _vp, _vp, _vp, _vp,
                                    ctypes.c_size_t, _vp])
-_sig("ig4_mrope_rotate", [ctypes.POINTER(Rotary), _vp, ctypes.c_longlong, ctypes.POINTER(Heads),
-                          ctypes.POINTER(Heads), ctypes.POINTER(Heads), ctypes.POINTER(Heads),
-                          _vp])
+_sig("ig4_mrope_rotate", [_vp, _vp, ctypes.c_longlong, _vp, _vp, _vp, _vp, _vp])
 _sig("ig4_nvfp4_matvec", [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp])
 _sig("ig4_nvfp4_swiglu_matvec", [_i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp])
 _sig("ig4_swiglu_backward_workspace_size", [_i, _i, _i], ctypes.c_size_t)
@@ -214,38 +213,39 @@ def _refuse(where: str):
     raise Ig4Error(IG4_ERR_INVALID_ARG, where)
 
 
-def _same_device(where: str, *tensors) -> int:
-    """Index of the current device, on which all the given tensors (None: absent) must lie."""
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            _refuse(where)
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            _refuse(where)
-    return dev
+def _device_of(where: str, t) -> int:
+    """Index of the tensor's device, which has to be the current one."""
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        _refuse(where)
+    return t.get_device()
 
 
-def _shaped(where: str, t, shape, *dtypes):
-    """Address of a dense tensor of this shape and one of these dtypes (None stays None)."""
+def _dense(where: str, dev: int, t, shape, *dtypes):
+    """Address of a dense tensor of this shape and one of these dtypes on device dev (None: None)."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes or not t.is_contiguous():
+    if t.get_device() != dev or t.shape != shape or t.dtype not in dtypes or \
+            not t.is_contiguous():
         _refuse(where)
     return t.data_ptr()
 
 
-def _workspace(where: str, workspace) -> tuple:
+def _scratch(where: str, dev: int, workspace) -> tuple:
     """(address, bytes) of a dense workspace tensor, or (None, 0)."""
     if workspace is None:
         return None, 0
-    if not workspace.is_contiguous():
+    if workspace.get_device() != dev or not workspace.is_contiguous():
         _refuse(where)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.nbytes
+
+
+# the current stream's handle without a Stream object around it, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _stream_on(dev: int, stream) -> int:
-    return (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def dtype_code(t: torch.Tensor) -> int:
@@ -560,6 +560,7 @@ def ig4_denoise_step(cfg: Config, cond: StackWeights, uncond: StackWeights, z, t
 # Ig4Error(IG4_ERR_INVALID_ARG) before the library is called.
 
 _FLOATS = (torch.float32, torch.bfloat16)
+_OUTPUTS = _FLOATS + (torch.float8_e4m3fn,)
 
 
 def ig4_add_rms_norm(x, r, g, eps, s_out, y_out, y_scale_out=None, y_sf_out=None, stream=None):
@@ -567,20 +568,20 @@ def ig4_add_rms_norm(x, r, g, eps, s_out, y_out, y_scale_out=None, y_sf_out=None
     s_out may be None.  An E4M3 y_out takes y_scale_out (fp32, one per row) or y_sf_out (uint8,
     MX8 block scales)."""
     name = "ig4_add_rms_norm"
-    dev = _same_device(name, x, r, g, s_out, y_out, y_scale_out, y_sf_out)
-    if x.dim() < 1 or x.numel() == 0:
+    dev = _device_of(name, x)
+    shape, dt, n = x.shape, x.dtype, x.numel()
+    if n == 0 or not shape:
         _refuse(name)
-    D = x.shape[-1]
-    M = x.numel() // D
+    D = shape[-1]
+    M = n // D
     if y_sf_out is not None and y_sf_out.numel() < ig4_mx8_scale_bytes(M, D):
         _refuse(name)
     _check(_lib.ig4_add_rms_norm(
-        M, D, _shaped(name, x, x.shape, *_FLOATS), _shaped(name, r, x.shape, x.dtype),
-        dtype_code(x), _shaped(name, g, (D,), torch.float32), eps,
-        _shaped(name, s_out, x.shape, x.dtype),
-        _shaped(name, y_out, x.shape, torch.float8_e4m3fn, *_FLOATS), dtype_code(y_out),
-        _shaped(name, y_scale_out, x.shape[:-1], torch.float32),
-        None if y_sf_out is None else _shaped(name, y_sf_out, y_sf_out.shape, torch.uint8),
+        M, D, _dense(name, dev, x, shape, *_FLOATS), _dense(name, dev, r, shape, dt),
+        _DTYPE_CODE[dt], _dense(name, dev, g, (D,), torch.float32), eps,
+        _dense(name, dev, s_out, shape, dt), _dense(name, dev, y_out, shape, *_OUTPUTS),
+        _DTYPE_CODE[y_out.dtype], _dense(name, dev, y_scale_out, shape[:-1], torch.float32),
+        None if y_sf_out is None else _dense(name, dev, y_sf_out, y_sf_out.shape, torch.uint8),
         _stream_on(dev, stream)), name)
 
 
@@ -592,30 +593,34 @@ def ig4_add_rms_norm_backward(s, g, eps, dy, ds, dx_out, dg_out, workspace=None,
     """Gradients of ig4_add_rms_norm: dx_out (of x and of r alike) and dg_out from dy and, unless
     None, ds, the gradient arriving at s.  dg_out None: frozen weight (no workspace needed)."""
     name = "ig4_add_rms_norm_backward"
-    dev = _same_device(name, s, g, dy, ds, dx_out, dg_out, workspace)
-    if s.dim() < 1 or s.numel() == 0:
+    dev = _device_of(name, s)
+    shape, dt, n = s.shape, s.dtype, s.numel()
+    if n == 0 or not shape:
         _refuse(name)
-    D = s.shape[-1]
-    ws, ws_bytes = _workspace(name, workspace)
+    D = shape[-1]
+    ws, ws_bytes = _scratch(name, dev, workspace)
     _check(_lib.ig4_add_rms_norm_backward(
-        s.numel() // D, D, _shaped(name, s, s.shape, *_FLOATS), dtype_code(s),
-        _shaped(name, g, (D,), torch.float32), eps, _shaped(name, dy, s.shape, *_FLOATS),
-        dtype_code(dy), _shaped(name, ds, s.shape, s.dtype),
-        _shaped(name, dx_out, s.shape, s.dtype), _shaped(name, dg_out, (D,), torch.float32),
+        n // D, D, _dense(name, dev, s, shape, *_FLOATS), _DTYPE_CODE[dt],
+        _dense(name, dev, g, (D,), torch.float32), eps, _dense(name, dev, dy, shape, *_FLOATS),
+        _DTYPE_CODE[dy.dtype], _dense(name, dev, ds, shape, dt),
+        _dense(name, dev, dx_out, shape, dt), _dense(name, dev, dg_out, (D,), torch.float32),
         ws, ws_bytes, _stream_on(dev, stream)), name)
 
 
-def _heads(where: str, t, like) -> Heads | None:
-    """The strided view of a [B, L, H, head_dim] tensor (elements of a head contiguous)."""
-    if t is None:
-        return None
-    B, L, H, d = t.shape if t.dim() == 4 else _refuse(where)
-    if (B, L, d) != (like.shape[0], like.shape[1], like.shape[3]) or t.dtype != like.dtype or \
-            (d > 1 and t.stride(3) != 1):
+# the C structs as packed bytes (building a ctypes.Structure takes ten times as long)
+_pack_rotary = struct.Struct("@4id7i4x").pack
+_pack_heads = struct.Struct("@Pi3q").pack
+
+
+def _heads(where: str, dev: int, t, B: int, L: int, d: int, dt):
+    """ig4_heads of a [B, L, H, d] view (elements of a head contiguous)."""
+    shape, strides = t.shape, t.stride()
+    if t.get_device() != dev or t.dtype != dt or len(shape) != 4 or shape[0] != B or \
+            shape[1] != L or shape[3] != d or (d > 1 and strides[3] != 1):
         _refuse(where)
     # a dimension of one element is never stepped over, whatever its stride says
-    sb, sl, sh = (st if n > 1 else 0 for n, st in zip(t.shape[:3], t.stride()[:3]))
-    return Heads(t.data_ptr(), H, sb, sl, sh)
+    return _pack_heads(t.data_ptr(), shape[2], strides[0] if B > 1 else 0,
+                       strides[1] if L > 1 else 0, strides[2] if shape[2] > 1 else 0)
 
 
 def ig4_mrope_rotate(q, k, pos, theta, sections, q_out, k_out, rotary_dim=None, interleaved=False,
@@ -624,56 +629,61 @@ def ig4_mrope_rotate(q, k, pos, theta, sections, q_out, k_out, rotary_dim=None, 
     their positions pos, int32 [3, L] or [B, 3, L]; q_out / k_out may be q / k.  rotary_dim
     defaults to twice the sum of sections; inverse=True rotates back (the gradient)."""
     name = "ig4_mrope_rotate"
-    dev = _same_device(name, q, k, pos, q_out, k_out)
-    if q.dim() != 4 or q.dtype not in _FLOATS or pos.dtype != torch.int32 or \
-            not pos.is_contiguous() or (k is None) != (k_out is None):
+    dev = _device_of(name, q)
+    if q.dim() != 4 or (k is None) != (k_out is None):
         _refuse(name)
-    B, L, _, d = q.shape
-    if tuple(pos.shape) not in ((3, L), (B, 3, L)):
-        _refuse(name)
-    rot = Rotary(B, L, d, 2 * sum(sections) if rotary_dim is None else rotary_dim, theta,
-                 (_i * 3)(*sections), int(interleaved), int(adjacent), int(inverse), dtype_code(q))
-    views = [_heads(name, t, q) for t in (q, q_out, k, k_out)]
-    _check(_lib.ig4_mrope_rotate(ctypes.byref(rot), pos.data_ptr(), 3 * L if pos.dim() == 3 else 0,
-                                 *(None if v is None else ctypes.byref(v) for v in views),
-                                 _stream_on(dev, stream)), name)
+    (B, L, _, d), dt = q.shape, q.dtype
+    shared = pos.dim() == 2
+    s0, s1, s2 = sections
+    _check(_lib.ig4_mrope_rotate(
+        _pack_rotary(B, L, d, 2 * (s0 + s1 + s2) if rotary_dim is None else rotary_dim, theta,
+                     s0, s1, s2, bool(interleaved), bool(adjacent), bool(inverse),
+                     _DTYPE_CODE.get(dt, -1)),
+        _dense(name, dev, pos, (3, L) if shared else (B, 3, L), torch.int32),
+        0 if shared else 3 * L, _heads(name, dev, q, B, L, d, dt),
+        _heads(name, dev, q_out, B, L, d, dt),
+        None if k is None else _heads(name, dev, k, B, L, d, dt),
+        None if k is None else _heads(name, dev, k_out, B, L, d, dt), _stream_on(dev, stream)),
+        name)
 
 
-def _nvfp4(where: str, codes, sf, scale, K: int) -> tuple:
+def _nvfp4(where: str, dev: int, codes, sf, scale, K: int) -> tuple:
     """Addresses of NVFP4 weights [N, K]: codes uint8 [N, K/2], packed scales, fp32 scale [N]."""
     N = codes.shape[0]
-    if sf.numel() < ig4_nvfp4_scale_bytes(N, K):
+    if sf.numel() < (N + 127) // 128 * 128 * K // 16:
         _refuse(where)
-    return (_shaped(where, codes, (N, K // 2), torch.uint8),
-            _shaped(where, sf, sf.shape, torch.uint8), _shaped(where, scale, (N,), torch.float32))
+    return (_dense(where, dev, codes, (N, K // 2), torch.uint8),
+            _dense(where, dev, sf, sf.shape, torch.uint8),
+            _dense(where, dev, scale, (N,), torch.float32))
 
 
 def ig4_nvfp4_matvec(x, w_codes, w_sf, w_scale, bias, out, stream=None):
     """out [M, N] (fp32 or bf16) = x [M, K] (bf16, M <= 8) times NVFP4 weights (+ bias)."""
     name = "ig4_nvfp4_matvec"
-    dev = _same_device(name, x, w_codes, w_sf, w_scale, bias, out)
+    dev = _device_of(name, x)
     if x.dim() != 2 or w_codes.dim() != 2:
         _refuse(name)
     (M, K), N = x.shape, w_codes.shape[0]
     _check(_lib.ig4_nvfp4_matvec(
-        M, N, K, _shaped(name, x, (M, K), torch.bfloat16), *_nvfp4(name, w_codes, w_sf, w_scale, K),
-        _shaped(name, bias, (N,), torch.float32), _shaped(name, out, (M, N), *_FLOATS),
-        dtype_code(out), _stream_on(dev, stream)), name)
+        M, N, K, _dense(name, dev, x, (M, K), torch.bfloat16),
+        *_nvfp4(name, dev, w_codes, w_sf, w_scale, K),
+        _dense(name, dev, bias, (N,), torch.float32), _dense(name, dev, out, (M, N), *_FLOATS),
+        _DTYPE_CODE[out.dtype], _stream_on(dev, stream)), name)
 
 
 def ig4_nvfp4_swiglu_matvec(x, gate_codes, gate_sf, gate_scale, up_codes, up_sf, up_scale, u_out,
                             stream=None):
     """u_out [M, I] bf16 = silu(x Wg^T) * (x Wu^T), x [M, K] bf16, M <= 8, NVFP4 weights."""
     name = "ig4_nvfp4_swiglu_matvec"
-    dev = _same_device(name, x, gate_codes, gate_sf, gate_scale, up_codes, up_sf, up_scale, u_out)
+    dev = _device_of(name, x)
     if x.dim() != 2 or gate_codes.dim() != 2 or up_codes.shape != gate_codes.shape:
         _refuse(name)
     (M, K), I = x.shape, gate_codes.shape[0]
     _check(_lib.ig4_nvfp4_swiglu_matvec(
-        M, I, K, _shaped(name, x, (M, K), torch.bfloat16),
-        *_nvfp4(name, gate_codes, gate_sf, gate_scale, K),
-        *_nvfp4(name, up_codes, up_sf, up_scale, K), _shaped(name, u_out, (M, I), torch.bfloat16),
-        _stream_on(dev, stream)), name)
+        M, I, K, _dense(name, dev, x, (M, K), torch.bfloat16),
+        *_nvfp4(name, dev, gate_codes, gate_sf, gate_scale, K),
+        *_nvfp4(name, dev, up_codes, up_sf, up_scale, K),
+        _dense(name, dev, u_out, (M, I), torch.bfloat16), _stream_on(dev, stream)), name)
 
 
 def ig4_swiglu_backward_workspace_size(M: int, I: int, K: int) -> int:
@@ -685,16 +695,16 @@ def ig4_swiglu_backward(h, w_gate, w_up, du, dh_out, dw_gate_out, dw_up_out, wor
     """Gradients of ig4_swiglu (bf16) from du: dh_out and dw_gate_out, dw_up_out (None: not
     wanted).  h [M, K], weights [I, K], du [M, I]."""
     name = "ig4_swiglu_backward"
-    dev = _same_device(name, h, w_gate, w_up, du, dh_out, dw_gate_out, dw_up_out, workspace)
+    dev = _device_of(name, h)
     if h.dim() != 2 or w_gate.dim() != 2:
         _refuse(name)
     (M, K), I, b = h.shape, w_gate.shape[0], torch.bfloat16
-    ws, ws_bytes = _workspace(name, workspace)
     _check(_lib.ig4_swiglu_backward(
-        M, I, K, _shaped(name, h, (M, K), b), _shaped(name, w_gate, (I, K), b),
-        _shaped(name, w_up, (I, K), b), _shaped(name, du, (M, I), b),
-        _shaped(name, dh_out, (M, K), b), _shaped(name, dw_gate_out, (I, K), b),
-        _shaped(name, dw_up_out, (I, K), b), ws, ws_bytes, _stream_on(dev, stream)), name)
+        M, I, K, _dense(name, dev, h, (M, K), b), _dense(name, dev, w_gate, (I, K), b),
+        _dense(name, dev, w_up, (I, K), b), _dense(name, dev, du, (M, I), b),
+        _dense(name, dev, dh_out, (M, K), b), _dense(name, dev, dw_gate_out, (I, K), b),
+        _dense(name, dev, dw_up_out, (I, K), b), *_scratch(name, dev, workspace),
+        _stream_on(dev, stream)), name)
 
 
 def ig4_last_device_error(stream=None) -> int:
