@@ -2697,55 +2697,60 @@ bool swiglu_grad_sizes_ok(int M, int I, int K) {
          K % 64 == 0 && K <= (1 << 17);
 }
 
-// Shares of dh's contraction.  With few output tiles most of the 74 CTA pairs
-// would idle, so the 2I-long contraction is cut into equal shares whose fp32
-// partial sums are added afterwards; a share costs the write and the read of
-// one fp32 M x K matrix.  Both sides in units of one k-block of a pair tile
-// (0.28 us): rounds * k-blocks of a share + 8 M K bytes per share at 5 TB/s.
-int swiglu_grad_shares(int M, int I, int K) {
-  const long tiles = static_cast<long>((M + 255) / 256) * ((K + 255) / 256);
-  const int kblocks = 2 * I / 64;
-  int best = 1;
-  double best_cost = 1e300;
-  for (int z = 1; z <= 16 && z <= kblocks; ++z) {
-    const long rounds = (tiles * z + 73) / 74;
-    const double cost = static_cast<double>(rounds) * ((kblocks + z - 1) / z + 4) +
-                        (z > 1 ? z * 8.0 * M * K / 1.4e6 + 10 : 0.0);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = z;
-    }
-  }
-  return best;
+// Work list of C [rows][N] over kblocks k-blocks on GRAD_PAIRS CTA pairs: what
+// is left of the tiles after whole rounds is cut into as many contraction shares
+// as give every pair at most one item (see GradPlan); `split` false: no shares
+// (short contractions).
+constexpr int GRAD_PAIRS = 74;
+GradPlan grad_plan(long rows, int N, int kblocks, int kb0, int split_row, bool split) {
+  GradPlan p{};
+  p.m_tiles = static_cast<int>((rows + 255) / 256);
+  p.n_tiles = (N + 255) / 256;
+  p.group_m = gemm_group_m(rows, 64L * kblocks, 2);
+  p.kblocks = kblocks;
+  p.kb0 = kb0;
+  p.rows = static_cast<int>(rows);
+  p.N = N;
+  p.split_row = split_row;
+  const int tiles = p.m_tiles * p.n_tiles, rest = tiles % GRAD_PAIRS;
+  p.full = tiles - rest;
+  p.shares = split && rest ? std::max(1, std::min({GRAD_PAIRS / rest, 16, kblocks})) : 1;
+  p.items = p.full + rest * p.shares;
+  return p;
+}
+size_t grad_part_bytes(const GradPlan &p) {
+  return p.shares > 1 ? static_cast<size_t>(p.items - p.full) * 65536 * 4 : 0;
+}
+GradPlan swiglu_dh_plan(int M, int I, int K) {
+  return grad_plan(M, K, 2 * I / 64, I / 64, M, true);
 }
 
 struct SwigluGradWs {
   __nv_bfloat16 *p;  // dG | dU [M][2I]
-  float *part;       // [shares][M][K]
+  float *part;       // dh's split tiles
   size_t bytes;
 };
 SwigluGradWs swiglu_grad_ws(int M, int I, int K, void *base) {
   SwigluGradWs w{};
   uint8_t *b = static_cast<uint8_t *>(base);
   const size_t pb = round_up(static_cast<size_t>(M) * 2 * I * 2, 256);
-  const int z = swiglu_grad_shares(M, I, K);
   w.p = reinterpret_cast<__nv_bfloat16 *>(b);
-  w.part = z > 1 ? reinterpret_cast<float *>(b + pb) : nullptr;
-  w.bytes = pb + (z > 1 ? round_up(static_cast<size_t>(z) * M * K * 4, 256) : 0);
+  w.part = reinterpret_cast<float *>(b + pb);
+  w.bytes = pb + grad_part_bytes(swiglu_dh_plan(M, I, K));
   return w;
 }
 
 template <bool A_MN>
 ig4_status launch_grad_gemm(const CUtensorMap &A, const CUtensorMap &B0, const CUtensorMap &B1,
-                            long rows, int N, int kblocks, int kb0, int shares, int group_m,
-                            const EpiGrad &epi, cudaStream_t st) {
+                            void *out0, void *out1, const GradPlan &p, cudaStream_t st) {
   DeviceInfo *di = nullptr;
   IG4_TRY(device_info(&di));
   auto kern = grad_pair_kernel<A_MN>;
   IG4_TRY(allow_smem(kern, GRAD_SMEM_BYTES));
-  const int m_tiles = static_cast<int>((rows + 255) / 256), n_tiles = (N + 255) / 256;
-  const long items = static_cast<long>(m_tiles) * n_tiles * shares;
-  const int pairs = static_cast<int>(std::min<long>(items, di->sms / 2));
+  CUtensorMap o0, o1;
+  IG4_TRY(map_2d(&o0, out0, 2, p.split_row, p.N, p.N, 32, 64));
+  IG4_TRY(map_2d(&o1, out1, 2, std::max(1, p.rows - p.split_row), p.N, p.N, 32, 64));
+  const int pairs = std::min({p.items, di->sms / 2, GRAD_PAIRS});
   cudaLaunchConfig_t lc = {};
   lc.gridDim = dim3(2 * pairs);
   lc.blockDim = dim3(GEMM_THREADS);
@@ -2760,9 +2765,7 @@ ig4_status launch_grad_gemm(const CUtensorMap &A, const CUtensorMap &B0, const C
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = attr;
   lc.numAttrs = 2;
-  if (cudaLaunchKernelEx(&lc, kern, A, B0, B1, m_tiles, n_tiles, kblocks, kb0, shares, group_m,
-                         epi) != cudaSuccess)
-    return IG4_ERR_CUDA;
+  if (cudaLaunchKernelEx(&lc, kern, A, B0, B1, o0, o1, p) != cudaSuccess) return IG4_ERR_CUDA;
   return last_launch_status();
 }
 
@@ -2984,21 +2987,16 @@ ig4_status ig4_swiglu_backward(int M, int I, int K, const void *h, const void *w
     IG4_TRY((launch_gemm<256, false, true>(ma, mg, mu, M, I / 128, K, e, st)));
   }
   if (dh_out) {
-    const int shares = swiglu_grad_shares(M, I, K);
+    GradPlan p = swiglu_dh_plan(M, I, K);
+    p.part = ws.part;
     CUtensorMap ma, mg, mu;
     IG4_TRY(map_2d(&ma, ws.p, 2, M, 2L * I, 2L * I, GEMM_BM, 64));
     IG4_TRY(map_mn_slabs(&mg, w_gate, I, K));
     IG4_TRY(map_mn_slabs(&mu, w_up, I, K));
-    const EpiGrad e{static_cast<__nv_bfloat16 *>(dh_out), nullptr, M,
-                    shares > 1 ? ws.part : nullptr, M, K};
-    IG4_TRY(launch_grad_gemm<false>(ma, mg, mu, M, K, 2 * I / 64, I / 64, shares,
-                                    gemm_group_m(M, 2L * I, 2), e, st));
-    if (shares > 1) {
-      const long n8 = static_cast<long>(M) * K / 8;
-      const int grid = static_cast<int>(std::min<long>((n8 + 255) / 256, 148 * 8));
-      if (launch_pdl(grad_reduce_kernel, dim3(grid), dim3(256), 0, st,
-                     reinterpret_cast<const float4 *>(ws.part), shares, n8,
-                     static_cast<uint4 *>(dh_out)) != cudaSuccess)
+    IG4_TRY(launch_grad_gemm<false>(ma, mg, mu, dh_out, dh_out, p, st));
+    if (p.shares > 1) {
+      if (launch_pdl(grad_reduce_kernel, dim3((p.items - p.full) / p.shares, 32), dim3(256), 0, st, p,
+                     static_cast<__nv_bfloat16 *>(dh_out)) != cudaSuccess)
         return IG4_ERR_CUDA;
       IG4_TRY(last_launch_status());
     }
@@ -3008,10 +3006,8 @@ ig4_status ig4_swiglu_backward(int M, int I, int K, const void *h, const void *w
     CUtensorMap ma, mb;
     IG4_TRY(map_mn_slabs(&ma, ws.p, M, 2L * I));
     IG4_TRY(map_mn_slabs(&mb, h, M, K));
-    const EpiGrad e{static_cast<__nv_bfloat16 *>(dw_gate_out),
-                    static_cast<__nv_bfloat16 *>(dw_up_out), I, nullptr, 2 * I, K};
-    IG4_TRY(launch_grad_gemm<true>(ma, mb, mb, 2L * I, K, kblocks, kblocks, 1,
-                                   gemm_group_m(2L * I, M, 2), e, st));
+    IG4_TRY(launch_grad_gemm<true>(ma, mb, mb, dw_gate_out, dw_up_out,
+                                   grad_plan(2L * I, K, kblocks, kblocks, I, false), st));
   }
   return IG4_OK;
 }

@@ -79,57 +79,88 @@ struct EpiSwiGLUGrad {
   }
 };
 
-// Output of the two gradient GEMMs: bf16 rows, rows at or past `split_row` in
-// a second matrix (dWg | dWu), or fp32 partial sums of contraction share z.
-struct EpiGrad {
-  __nv_bfloat16 *out0, *out1;
-  int split_row;
-  float *part;  // != nullptr: [shares][rows][N] fp32 partial sums instead
-  int rows, N;
+// Tiled TMA store of a box in shared memory (clipped at the tensor's ends)
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, const void *src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the latest N of this thread's bulk stores have read their source
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
 
-  __device__ __forceinline__ void operator()(int m0, int n0, int z, uint32_t tacc, int r) const {
-    const int row = m0 + r;
-    const bool valid = row < rows;
-    __nv_bfloat16 *o = row < split_row ? out0 + static_cast<long>(row) * N
-                                       : out1 + static_cast<long>(row - split_row) * N;
-    float *pf = part + (static_cast<long>(z) * rows + row) * N;
-#pragma unroll 1
-    for (int c = 0; c < 256; c += 32) {
-      float v[32];
-      tmem_ld32(tacc + c, v);
-      tmem_ld_wait();
-      if (!valid || n0 + c >= N) continue;
-      if (part != nullptr)
-        store32_f32(pf + n0 + c, v);
-      else
-        store32_bf16(o + n0 + c, v);
+// Work of a gradient GEMM.  Tiles 0 .. full - 1, a multiple of the pairs, are
+// whole items.  The rest would leave most pairs idle for a whole tile's time,
+// so each is cut along the contraction into `shares` items whose fp32 sums go to
+// part [tile - full][share][256][256] and are added by grad_reduce_kernel.
+struct GradPlan {
+  int m_tiles, n_tiles, group_m;
+  int full, shares, items;
+  int kblocks, kb0;  // the contraction runs over B0 for kb0 k-blocks, then over B1
+  int rows, N;       // of the output; rows from split_row on go to the second map
+  int split_row;
+  float *part;
+};
+struct GradItem {
+  int mt, nt, share, b0, nkb;  // tile, contraction share (-1: whole), first k-block, k-blocks
+};
+__device__ __forceinline__ GradItem grad_item(const GradPlan &p, int t) {
+  GradItem i;
+  int tile = t;
+  i.share = -1;
+  i.b0 = 0;
+  i.nkb = p.kblocks;
+  if (t >= p.full) {
+    const int e = t - p.full;
+    tile = p.full + e / p.shares;
+    if (p.shares > 1) {
+      i.share = e % p.shares;
+      i.b0 = static_cast<int>(static_cast<long>(p.kblocks) * i.share / p.shares);
+      i.nkb = static_cast<int>(static_cast<long>(p.kblocks) * (i.share + 1) / p.shares) - i.b0;
     }
   }
-};
+  tile_coords(tile, p.m_tiles, p.n_tiles, p.group_m, &i.mt, &i.nt);
+  return i;
+}
 
 // C = A B on CTA pairs, B MN-major, A K-major (dh) or MN-major (dW).
 // A K-major: tmA maps A [rows][contraction] in boxes of 128 rows x 64; MN-major
 // operands: 3-D maps {64 elements, contraction rows, slabs of 64 elements} in
-// boxes {64, 64, 2}.  The contraction runs over tmB0 for the first kb0 k-blocks
-// and over tmB1 after them.  An item is an output tile of 256 x 256 and one of
-// `shares` equal runs of k-blocks; pairs take items round-robin.  Roles,
-// barriers and the two TMEM accumulators are those of gemm_pair_kernel.
+// boxes {64, 64, 2}.  Roles, barriers and the two TMEM accumulators are those of
+// gemm_pair_kernel.
+//
+// The results leave through shared memory by TMA stores, 64 columns at a time:
+// a lane holds a row of the accumulator, and storing its 64 bytes directly, row
+// after row 2 N bytes apart, took 13,000 cycles a tile, more than the MMAs of a
+// tile take below 1600 tokens.
 constexpr int GRAD_STAGES = 6;
 constexpr int GRAD_STAGE_BYTES = 2 * 16384;
-constexpr int GRAD_SMEM_BYTES = GRAD_STAGES * GRAD_STAGE_BYTES + 1024 + 256;
+constexpr int GRAD_OUT_BYTES = 32 * 128;  // 32 rows x 64 columns; two per epilogue warp
+constexpr int GRAD_SMEM_BYTES =
+    GRAD_STAGES * GRAD_STAGE_BYTES + 8 * GRAD_OUT_BYTES + 1024 + 256;
 
 template <bool A_MN>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
     grad_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
-                     const __grid_constant__ CUtensorMap tmB1, int m_tiles, int n_tiles, int kblocks,
-                     int kb0, int shares, int group_m, const EpiGrad epi) {
+                     const __grid_constant__ CUtensorMap tmB1, const __grid_constant__ CUtensorMap tmO0,
+                     const __grid_constant__ CUtensorMap tmO1, const GradPlan p) {
   constexpr uint32_t IDESC = idesc_bf16_major(2 * GEMM_BM, 256, A_MN, true);
   constexpr uint32_t TMEM_COLS = 512;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = align1024(smem_raw);
   uint8_t *sA = smem;
   uint8_t *sB = smem + GRAD_STAGES * 16384;
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + GRAD_STAGES * GRAD_STAGE_BYTES);
+  uint8_t *sO = smem + GRAD_STAGES * GRAD_STAGE_BYTES;
+  uint64_t *full = reinterpret_cast<uint64_t *>(sO + 8 * GRAD_OUT_BYTES);
   uint64_t *empty = full + GRAD_STAGES;
   uint64_t *tfull = empty + GRAD_STAGES;
   uint64_t *tempty = tfull + 2;
@@ -142,8 +173,6 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1;
   const int n_pairs = gridDim.x >> 1;
-  const int tiles = m_tiles * n_tiles;
-  const int items = tiles * shares;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < GRAD_STAGES; ++s) {
@@ -162,6 +191,8 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB0);
     tma_prefetch_desc(&tmB1);
+    tma_prefetch_desc(&tmO0);
+    tma_prefetch_desc(&tmO1);
   }
   if (warp == 5) {
     tmem_alloc_pair(tmem_slot, TMEM_COLS);
@@ -174,38 +205,32 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   pdl_wait();
   pdl_trigger();
 
-  // k-blocks [first, last) of share z (none empty: shares <= kblocks)
-  auto share_begin = [&](int z) { return static_cast<int>(static_cast<long>(kblocks) * z / shares); };
-
   if (warp == 4) {
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 0;
       bool ok = true;
       int local = 0;
-      for (int t = pair; t < items && ok; t += n_pairs, ++local) {
-        int mt, nt;
-        const int z = t / tiles;
-        tile_coords(t - z * tiles, m_tiles, n_tiles, group_m, &mt, &nt);
-        const int b0 = share_begin(z), nkb = share_begin(z + 1) - b0;
-        for (int it = 0; it < nkb; ++it) {
-          const int kb = b0 + ((local & 1) ? nkb - 1 - it : it);  // K-snake
+      for (int t = pair; t < p.items && ok; t += n_pairs, ++local) {
+        const GradItem w = grad_item(p, t);
+        for (int it = 0; it < w.nkb; ++it) {
+          const int kb = w.b0 + ((local & 1) ? w.nkb - 1 - it : it);  // K-snake
           if (!mbar_wait_cluster(&empty[s], ph ^ 1, abort_flag)) {
             ok = false;
             break;
           }
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * GRAD_STAGE_BYTES);
           const uint32_t bar = map_shared_to_rank(&full[s], 0);
-          const int am = mt * 2 * GEMM_BM + static_cast<int>(rank) * GEMM_BM;
+          const int am = w.mt * 2 * GEMM_BM + static_cast<int>(rank) * GEMM_BM;
           if constexpr (A_MN)
             tma_load_3d_pair(sA + s * 16384, &tmA, bar, 0, kb * 64, am / 64);
           else
             tma_load_2d_pair(sA + s * 16384, &tmA, bar, kb * 64, am);
-          const int bn = (nt * 256 + static_cast<int>(rank) * 128) / 64;
-          if (kb < kb0)
+          const int bn = (w.nt * 256 + static_cast<int>(rank) * 128) / 64;
+          if (kb < p.kb0)
             tma_load_3d_pair(sB + s * 16384, &tmB0, bar, 0, kb * 64, bn);
           else
-            tma_load_3d_pair(sB + s * 16384, &tmB1, bar, 0, (kb - kb0) * 64, bn);
+            tma_load_3d_pair(sB + s * 16384, &tmB1, bar, 0, (kb - p.kb0) * 64, bn);
           if (++s == GRAD_STAGES) {
             s = 0;
             ph ^= 1;
@@ -220,14 +245,13 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       uint32_t ph = 0;
       int local = 0;
       bool ok = true;
-      for (int t = pair; t < items && ok; t += n_pairs, ++local) {
+      for (int t = pair; t < p.items && ok; t += n_pairs, ++local) {
         const int buf = local & 1;
         const uint32_t use = static_cast<uint32_t>(local >> 1);
         if (!mbar_wait_cluster(&tempty[buf], (use & 1) ^ 1, abort_flag)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + buf * 256;
-        const int z = t / tiles;
-        const int nkb = share_begin(z + 1) - share_begin(z);
+        const int nkb = grad_item(p, t).nkb;
         for (int it = 0; it < nkb; ++it) {
           if (!mbar_wait_cluster(&full[s], ph, abort_flag)) {
             ok = false;
@@ -255,26 +279,73 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
       mbar_wait_cluster(drain, 0, nullptr, WAIT_LIMIT_NS / 4);
     }
   } else {
-    const int r = warp * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t tempty_leader0 = map_shared_to_rank(&tempty[0], 0);
     const uint32_t tempty_leader1 = map_shared_to_rank(&tempty[1], 0);
-    int local = 0;
-    for (int t = pair; t < items; t += n_pairs, ++local) {
+    uint8_t *out = sO + warp * 2 * GRAD_OUT_BYTES;  // 1024-byte aligned: the swizzle's period
+    int local = 0, slot = 0;
+    for (int t = pair; t < p.items; t += n_pairs, ++local) {
       const int buf = local & 1;
       const uint32_t use = static_cast<uint32_t>(local >> 1);
       const bool ok = mbar_wait_cluster(&tfull[buf], use & 1, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      int mt, nt;
-      const int z = t / tiles;
-      tile_coords(t - z * tiles, m_tiles, n_tiles, group_m, &mt, &nt);
-      epi(mt * 2 * GEMM_BM + static_cast<int>(rank) * GEMM_BM, nt * 256, z,
-          tmem_base + lane_base + buf * 256, r);
+      const GradItem w = grad_item(p, t);
+      const uint32_t tacc = tmem_base + lane_base + buf * 256;
+      const int n0 = w.nt * 256;
+      const int row0 = w.mt * 2 * GEMM_BM + static_cast<int>(rank) * GEMM_BM + warp * 32;
+      if (w.share >= 0) {
+        const int tile = (t - p.full) / p.shares;
+        float *dst = p.part + ((static_cast<long>(tile) * p.shares + w.share) * 256 +
+                               rank * GEMM_BM + warp * 32 + lane) * 256;
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 32) {
+          float v[32];
+          tmem_ld32(tacc + c, v);
+          tmem_ld_wait();
+          if (row0 + lane < p.rows && n0 + c < p.N) store32_f32(dst + c, v);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 64) {
+          float v[32], u[32];
+          tmem_ld32(tacc + c, v);
+          tmem_ld32(tacc + c + 32, u);
+          tmem_ld_wait();
+          if (n0 + c >= p.N || row0 >= p.rows) continue;  // (uniform in the warp)
+          uint8_t *o = out + slot * GRAD_OUT_BYTES;
+          if (lane == 0) bulk_wait_read<1>();  // the store before last has read this slot
+          __syncwarp();
+          // row `lane`, 16-byte chunk q at q ^ (row % 8): the 128-byte swizzle
+          uint8_t *orow = o + lane * 128;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            *reinterpret_cast<uint4 *>(orow + ((q ^ (lane & 7)) << 4)) =
+                make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                           pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                           pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+            *reinterpret_cast<uint4 *>(orow + (((q + 4) ^ (lane & 7)) << 4)) =
+                make_uint4(pack_bf16x2(u[8 * q], u[8 * q + 1]), pack_bf16x2(u[8 * q + 2], u[8 * q + 3]),
+                           pack_bf16x2(u[8 * q + 4], u[8 * q + 5]),
+                           pack_bf16x2(u[8 * q + 6], u[8 * q + 7]));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < p.split_row)
+              tma_store_2d(&tmO0, o, n0 + c, row0);
+            else
+              tma_store_2d(&tmO1, o, n0 + c, row0 - p.split_row);
+            bulk_commit();
+          }
+          slot ^= 1;
+        }
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(buf ? tempty_leader1 : tempty_leader0);
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   __syncwarp();
@@ -284,22 +355,28 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   if (warp == 5) tmem_dealloc_pair(tmem_base, TMEM_COLS);
 }
 
-// out[i] = bf16 of the sum of `shares` fp32 partials, in share order; n8 vectors of 8
-__global__ void __launch_bounds__(256)
-    grad_reduce_kernel(const float4 *part, int shares, long n8, uint4 *out) {
+// The split tiles' sums: out = bf16 of the sum of a tile's partials, in share
+// order.  Grid (split tiles, 32): a CTA takes 8 rows of a tile, a thread 8
+// columns of one row.
+__global__ void __launch_bounds__(256) grad_reduce_kernel(const GradPlan p, __nv_bfloat16 *out) {
   pdl_wait();
   pdl_trigger();
-  for (long i = blockIdx.x * static_cast<long>(blockDim.x) + threadIdx.x; i < n8;
-       i += static_cast<long>(gridDim.x) * blockDim.x) {
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    for (int z = 0; z < shares; ++z) {
-      const float4 p = part[(z * n8 + i) * 2], q = part[(z * n8 + i) * 2 + 1];
-      a.x += p.x; a.y += p.y; a.z += p.z; a.w += p.w;
-      b.x += q.x; b.y += q.y; b.z += q.z; b.w += q.w;
-    }
-    out[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
-                        pack_bf16x2(b.z, b.w));
+  int mt, nt;
+  tile_coords(p.full + blockIdx.x, p.m_tiles, p.n_tiles, p.group_m, &mt, &nt);
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), c = (threadIdx.x & 31) * 8;
+  const int row = mt * 256 + r, col = nt * 256 + c;
+  if (row >= p.rows || col >= p.N) return;
+  const float *src = p.part + (static_cast<long>(blockIdx.x) * p.shares * 256 + r) * 256 + c;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+  for (int z = 0; z < p.shares; ++z) {
+    const float4 u = *reinterpret_cast<const float4 *>(src + static_cast<long>(z) * 65536);
+    const float4 v = *reinterpret_cast<const float4 *>(src + static_cast<long>(z) * 65536 + 4);
+    a.x += u.x; a.y += u.y; a.z += u.z; a.w += u.w;
+    b.x += v.x; b.y += v.y; b.z += v.z; b.w += v.w;
   }
+  *reinterpret_cast<uint4 *>(out + static_cast<long>(row) * p.N + col) =
+      make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                 pack_bf16x2(b.z, b.w));
 }
 
 }  // namespace ig4
