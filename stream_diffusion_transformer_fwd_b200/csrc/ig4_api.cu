@@ -2725,6 +2725,34 @@ GradPlan swiglu_dh_plan(int M, int I, int K) {
   return grad_plan(M, K, 2 * I / 64, I / 64, M, true);
 }
 
+// Up to 128 tokens: the plans of G^T, U^T and of dh^T (see GradRowsPlan).
+constexpr int GRAD_SMS = 148;
+constexpr int GRAD_ROWS_MAX_M = 128;
+GradRowsPlan grad_rows_plan(bool dh, int M, int I, int K) {
+  GradRowsPlan p{};
+  p.M = M;
+  p.I = I;
+  p.K = K;
+  p.nt = (M + 15) / 16 * 16;
+  p.stages = (GRAD_ROWS_SMEM - 1024) / grad_rows_stage_bytes(dh, p.nt);
+  p.shares = 1;
+  if (dh) {
+    p.R = 128;
+    p.tiles = (K + 127) / 128;
+    p.kblocks = 2 * I / 64;
+    p.kb0 = I / 64;
+    // shares of at least 8 k-blocks
+    p.shares = std::max(1, std::min({GRAD_SMS / p.tiles, 16, p.kblocks / 8}));
+  } else {
+    const int rounds = (I + 128 * GRAD_SMS - 1) / (128 * GRAD_SMS);
+    p.R = std::min(128, ((I + GRAD_SMS * rounds - 1) / (GRAD_SMS * rounds) + 7) / 8 * 8);
+    p.tiles = (I + p.R - 1) / p.R;
+    p.kblocks = p.kb0 = K / 64;
+  }
+  p.items = p.tiles * p.shares;
+  return p;
+}
+
 struct SwigluGradWs {
   __nv_bfloat16 *p;  // dG | dU [M][2I]
   float *part;       // dh's split tiles
@@ -2736,7 +2764,12 @@ SwigluGradWs swiglu_grad_ws(int M, int I, int K, void *base) {
   const size_t pb = round_up(static_cast<size_t>(M) * 2 * I * 2, 256);
   w.p = reinterpret_cast<__nv_bfloat16 *>(b);
   w.part = reinterpret_cast<float *>(b + pb);
-  w.bytes = pb + grad_part_bytes(swiglu_dh_plan(M, I, K));
+  if (M <= GRAD_ROWS_MAX_M) {
+    const int z = grad_rows_plan(true, M, I, K).shares;
+    w.bytes = pb + (z > 1 ? round_up(static_cast<size_t>(z) * M * K * 4, 256) : 0);
+  } else {
+    w.bytes = pb + grad_part_bytes(swiglu_dh_plan(M, I, K));
+  }
   return w;
 }
 
@@ -2766,6 +2799,48 @@ ig4_status launch_grad_gemm(const CUtensorMap &A, const CUtensorMap &B0, const C
   lc.attrs = attr;
   lc.numAttrs = 2;
   if (cudaLaunchKernelEx(&lc, kern, A, B0, B1, o0, o1, p) != cudaSuccess) return IG4_ERR_CUDA;
+  return last_launch_status();
+}
+
+template <bool DH>
+ig4_status launch_grad_rows(const CUtensorMap &A0, const CUtensorMap &A1, const CUtensorMap &B,
+                            const GradRowsPlan &p, const void *du, void *out, float *part,
+                            cudaStream_t st) {
+  DeviceInfo *di = nullptr;
+  IG4_TRY(device_info(&di));
+  auto kern = grad_rows_kernel<DH>;
+  const int smem = p.stages * grad_rows_stage_bytes(DH, p.nt) + 1024;
+  IG4_TRY(allow_smem(kern, smem));
+  if (launch_pdl(kern, dim3(std::min(p.items, di->sms)), dim3(GEMM_THREADS), smem, st, A0, A1, B, p,
+                 static_cast<const __nv_bfloat16 *>(du), static_cast<__nv_bfloat16 *>(out),
+                 part) != cudaSuccess)
+    return IG4_ERR_CUDA;
+  return last_launch_status();
+}
+
+// dG | dU and dh for up to GRAD_ROWS_MAX_M tokens
+ig4_status launch_swiglu_grad_rows(int M, int I, int K, const void *h, const void *w_gate,
+                                   const void *w_up, const void *du, void *dh,
+                                   const SwigluGradWs &ws, cudaStream_t st) {
+  CUtensorMap a0, a1, b;
+  GradRowsPlan p = grad_rows_plan(false, M, I, K);
+  IG4_TRY(map_2d(&a0, w_gate, 2, I, K, K, p.R, 64));
+  IG4_TRY(map_2d(&a1, w_up, 2, I, K, K, p.R, 64));
+  IG4_TRY(map_2d(&b, h, 2, M, K, K, p.nt, 64));
+  IG4_TRY(launch_grad_rows<false>(a0, a1, b, p, du, ws.p, nullptr, st));
+  if (!dh) return IG4_OK;
+  p = grad_rows_plan(true, M, I, K);
+  IG4_TRY(map_mn_slabs(&a0, w_gate, I, K));
+  IG4_TRY(map_mn_slabs(&a1, w_up, I, K));
+  IG4_TRY(map_2d(&b, ws.p, 2, M, 2L * I, 2L * I, p.nt, 64));
+  IG4_TRY(launch_grad_rows<true>(a0, a1, b, p, nullptr, dh, ws.part, st));
+  if (p.shares == 1) return IG4_OK;
+  const long n8 = static_cast<long>(M) * K / 8;
+  const int grid = static_cast<int>(std::min<long>((n8 + 255) / 256, GRAD_SMS * 8));
+  if (launch_pdl(grad_rows_reduce_kernel, dim3(grid), dim3(256), 0, st,
+                 reinterpret_cast<const float4 *>(ws.part), p.shares, n8,
+                 static_cast<uint4 *>(dh)) != cudaSuccess)
+    return IG4_ERR_CUDA;
   return last_launch_status();
 }
 
@@ -2978,7 +3053,10 @@ ig4_status ig4_swiglu_backward(int M, int I, int K, const void *h, const void *w
   const Span out[] = {{dh_out, hb}, {dw_gate_out, wb}, {dw_up_out, wb}, {workspace, ws.bytes}};
   if (!spans_ok(in, 4, out, 4, [](int, int) { return false; })) return IG4_ERR_INVALID_ARG;
   cudaStream_t st = as_stream(stream);
-  {
+  const bool few = M <= GRAD_ROWS_MAX_M;
+  if (few) {
+    IG4_TRY(launch_swiglu_grad_rows(M, I, K, h, w_gate, w_up, du, dh_out, ws, st));
+  } else {
     CUtensorMap ma, mg, mu;
     IG4_TRY(map_2d(&ma, h, 2, M, K, K, GEMM_BM, 64));
     IG4_TRY(map_2d(&mg, w_gate, 2, I, K, K, 128, 64));
@@ -2986,7 +3064,7 @@ ig4_status ig4_swiglu_backward(int M, int I, int K, const void *h, const void *w
     const EpiSwiGLUGrad e{static_cast<const __nv_bfloat16 *>(du), ws.p, I, M};
     IG4_TRY((launch_gemm<256, false, true>(ma, mg, mu, M, I / 128, K, e, st)));
   }
-  if (dh_out) {
+  if (dh_out && !few) {
     GradPlan p = swiglu_dh_plan(M, I, K);
     p.part = ws.part;
     CUtensorMap ma, mg, mu;

@@ -43,6 +43,14 @@ __host__ __device__ constexpr uint32_t idesc_bf16_major(int M, int N, bool a_mn,
   return idesc_bf16(M, N) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u);
 }
 
+// dG and dU of one element
+__device__ __forceinline__ void swiglu_grad(float g, float u, float du, float *dg, float *dup) {
+  const float sig = 1.0f / (1.0f + __expf(-g));
+  const float a = du * sig;
+  *dg = a * u * fmaf(g, 1.0f - sig, 1.0f);
+  *dup = a * g;
+}
+
 // Epilogue of the recomputation: accumulator columns [0,128) hold G, [128,256)
 // hold U of output columns n .. n + 127; writes dG to p[row][n..] and dU to
 // p[row][I + n..].
@@ -66,11 +74,7 @@ struct EpiSwiGLUGrad {
       load32_bf16(du + static_cast<long>(row) * I + n + c, d);
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        const float sig = 1.0f / (1.0f + __expf(-g[i]));
-        const float a = d[i] * sig;
-        const float dg = a * up[i] * fmaf(g[i], 1.0f - sig, 1.0f);
-        up[i] = a * g[i];
-        g[i] = dg;
+        swiglu_grad(g[i], up[i], d[i], &g[i], &up[i]);
       }
       __nv_bfloat16 *dst = p + static_cast<long>(row) * 2 * I + n + c;
       store32_bf16(dst, g);
@@ -144,9 +148,10 @@ __device__ __forceinline__ GradItem grad_item(const GradPlan &p, int t) {
 // tile take below 1600 tokens.
 constexpr int GRAD_STAGES = 6;
 constexpr int GRAD_STAGE_BYTES = 2 * 16384;
-constexpr int GRAD_OUT_BYTES = 32 * 128;  // 32 rows x 64 columns; two per epilogue warp
+constexpr int GRAD_OUT_BYTES = 32 * 128;  // 32 rows x 64 columns
+constexpr int GRAD_OUT_SLOTS = 2;         // per epilogue warp
 constexpr int GRAD_SMEM_BYTES =
-    GRAD_STAGES * GRAD_STAGE_BYTES + 8 * GRAD_OUT_BYTES + 1024 + 256;
+    GRAD_STAGES * GRAD_STAGE_BYTES + 4 * GRAD_OUT_SLOTS * GRAD_OUT_BYTES + 1024 + 256;
 
 template <bool A_MN>
 __global__ void __launch_bounds__(GEMM_THREADS, 1)
@@ -160,7 +165,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
   uint8_t *sA = smem;
   uint8_t *sB = smem + GRAD_STAGES * 16384;
   uint8_t *sO = smem + GRAD_STAGES * GRAD_STAGE_BYTES;
-  uint64_t *full = reinterpret_cast<uint64_t *>(sO + 8 * GRAD_OUT_BYTES);
+  uint64_t *full = reinterpret_cast<uint64_t *>(sO + 4 * GRAD_OUT_SLOTS * GRAD_OUT_BYTES);
   uint64_t *empty = full + GRAD_STAGES;
   uint64_t *tfull = empty + GRAD_STAGES;
   uint64_t *tempty = tfull + 2;
@@ -282,7 +287,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t tempty_leader0 = map_shared_to_rank(&tempty[0], 0);
     const uint32_t tempty_leader1 = map_shared_to_rank(&tempty[1], 0);
-    uint8_t *out = sO + warp * 2 * GRAD_OUT_BYTES;  // 1024-byte aligned: the swizzle's period
+    uint8_t *out = sO + warp * GRAD_OUT_SLOTS * GRAD_OUT_BYTES;  // 1024-byte aligned: the swizzle's period
     int local = 0, slot = 0;
     for (int t = pair; t < p.items; t += n_pairs, ++local) {
       const int buf = local & 1;
@@ -314,7 +319,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           tmem_ld_wait();
           if (n0 + c >= p.N || row0 >= p.rows) continue;  // (uniform in the warp)
           uint8_t *o = out + slot * GRAD_OUT_BYTES;
-          if (lane == 0) bulk_wait_read<1>();  // the store before last has read this slot
+          if (lane == 0) bulk_wait_read<GRAD_OUT_SLOTS - 1>();  // this slot's last store has read it
           __syncwarp();
           // row `lane`, 16-byte chunk q at q ^ (row % 8): the 128-byte swizzle
           uint8_t *orow = o + lane * 128;
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
               tma_store_2d(&tmO1, o, n0 + c, row0 - p.split_row);
             bulk_commit();
           }
-          slot ^= 1;
+          if (++slot == GRAD_OUT_SLOTS) slot = 0;
         }
       }
       tc_fence_before();
@@ -377,6 +382,233 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradPlan p, __nv
   *reinterpret_cast<uint4 *>(out + static_cast<long>(row) * p.N + col) =
       make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
                  pack_bf16x2(b.z, b.w));
+}
+
+// ------------------------------------------------------- up to 128 tokens
+// With few tokens the weights' bytes bound the first two products.  Tokens as the
+// MMA's 128 or 256 rows would spend most of it on empty rows (26 us of MMAs for 17
+// tokens at full width, as much as the bytes take), so here the weights are the
+// 128-row operand and the tokens, rounded up to 16, its columns.
+//   G^T, U^T (DH false): a CTA takes R rows of both weights, R chosen so that the
+//     CTAs cover all SMs evenly; the MMA's rows past R compute on what the stage
+//     holds there, and nothing reads them.
+//   dh^T (DH true): A is W MN-major, 128 of its columns; the contraction over 2I
+//     is cut into shares, whose fp32 sums [share][M][K] grad_rows_reduce_kernel
+//     adds (none with one share).
+struct GradRowsPlan {
+  int tiles, R;      // output tiles; weight rows (DH: columns, 128) of each
+  int nt;            // tokens rounded up to 16
+  int shares, items;
+  int kblocks, kb0;  // as in GradPlan
+  int stages;
+  int M, I, K;
+};
+constexpr int GRAD_ROWS_SMEM = 220 << 10;
+__host__ __device__ constexpr int grad_rows_stage_bytes(bool dh, int nt) {
+  return (dh ? 16384 : 32768) + nt * 128;
+}
+
+template <bool DH>
+__global__ void __launch_bounds__(GEMM_THREADS, 1)
+    grad_rows_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
+                     const __grid_constant__ CUtensorMap tmB, const GradRowsPlan p,
+                     const __nv_bfloat16 *du, __nv_bfloat16 *out, float *part) {
+  constexpr uint32_t TMEM_COLS = DH ? 128 : 256;
+  constexpr int B_OFF = DH ? 16384 : 32768;
+  constexpr int MAX_STAGES = 13;  // 220 KB / (16 KB + 16 tokens)
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align1024(smem_raw);
+  const int stage_bytes = grad_rows_stage_bytes(DH, p.nt);
+  __shared__ uint64_t full[MAX_STAGES], empty[MAX_STAGES], tfull, tempty, drain;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_word;
+  volatile int *abort_flag = &abort_word;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(&tfull, 1);
+    mbar_init(&tempty, 128);
+    mbar_init(&drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 4 && lane == 0) {
+    tma_prefetch_desc(&tmA0);
+    tma_prefetch_desc(&tmA1);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 5) {
+    tmem_alloc(&tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  pdl_wait();
+  pdl_trigger();
+
+  // item t: tile t / shares, k-blocks [first, last) of share t % shares
+  auto first_kb = [&](int z) { return static_cast<int>(static_cast<long>(p.kblocks) * z / p.shares); };
+
+  if (warp == 4) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 0;
+      long issued = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < p.items && ok; t += gridDim.x) {
+        const int tile = t / p.shares, z = t % p.shares;
+        for (int kb = first_kb(z); kb < first_kb(z + 1); ++kb) {
+          if (!mbar_wait(&empty[s], ph ^ 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t *st = smem + s * stage_bytes;
+          if constexpr (DH) {
+            mbar_arrive_expect_tx(&full[s], stage_bytes);
+            if (kb < p.kb0)
+              tma_load_3d(st, &tmA0, &full[s], 0, kb * 64, tile * 2);
+            else
+              tma_load_3d(st, &tmA1, &full[s], 0, (kb - p.kb0) * 64, tile * 2);
+          } else {
+            mbar_arrive_expect_tx(&full[s], (2 * p.R + p.nt) * 128);
+            tma_load_2d(st, &tmA0, &full[s], kb * 64, tile * p.R);
+            tma_load_2d(st + 16384, &tmA1, &full[s], kb * 64, tile * p.R);
+          }
+          tma_load_2d(st + B_OFF, &tmB, &full[s], kb * 64, 0);
+          ++issued;
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      if (!ok) {
+        // Let the loads already issued land before the CTA's shared memory goes away.
+        for (long i = (issued > p.stages ? issued - p.stages : 0); i < issued; ++i)
+          mbar_wait(&full[i % p.stages], static_cast<uint32_t>((i / p.stages) & 1), nullptr,
+                    WAIT_LIMIT_NS / 4);
+      }
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      const uint32_t idesc = idesc_bf16_major(128, p.nt, DH, false);
+      int s = 0;
+      uint32_t ph = 0;
+      uint32_t local = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < p.items && ok; t += gridDim.x, ++local) {
+        const int z = t % p.shares;
+        if (!mbar_wait(&tempty, (local & 1) ^ 1, abort_flag)) break;
+        tc_fence_after();
+        const int b0 = first_kb(z), nkb = first_kb(z + 1) - b0;
+        for (int it = 0; it < nkb; ++it) {
+          if (!mbar_wait(&full[s], ph, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_base = smem_u32(smem + s * stage_bytes);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t bd = sdesc_kmajor_sw128(a_base + B_OFF + kk * 32);
+            if constexpr (DH) {
+              umma_bf16(tmem_base, sdesc_mnmajor_sw128(a_base + kk * 2048), bd, idesc, (it | kk) != 0);
+            } else {
+              umma_bf16(tmem_base, sdesc_kmajor_sw128(a_base + kk * 32), bd, idesc, (it | kk) != 0);
+              umma_bf16(tmem_base + 128, sdesc_kmajor_sw128(a_base + 16384 + kk * 32), bd, idesc,
+                        (it | kk) != 0);
+            }
+          }
+          umma_commit(&empty[s]);
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) umma_commit(&tfull);
+      }
+      // Every MMA issued above has finished once `drain` completes.
+      umma_commit(&drain);
+      mbar_wait(&drain, 0, nullptr, WAIT_LIMIT_NS / 4);
+    }
+  } else {
+    const int r = warp * 32 + lane;
+    const uint32_t tacc = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
+    uint32_t local = 0;
+    for (int t = blockIdx.x; t < p.items; t += gridDim.x, ++local) {
+      if (!mbar_wait_warp(&tfull, local & 1, abort_flag)) break;
+      tc_fence_after();
+      const int tile = t / p.shares, z = t % p.shares;
+      const int n = tile * p.R + r;  // weight row (DH: column) of this lane
+      const bool valid = r < p.R && n < (DH ? p.K : p.I);
+#pragma unroll 1
+      for (int c = 0; c < p.nt; c += 32) {  // tokens c .. c + 31
+        float g[32];
+        tmem_ld32(tacc + c, g);
+        if constexpr (DH) {
+          tmem_ld_wait();
+          if (!valid) continue;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (c + i >= p.M) break;
+            if (p.shares > 1)
+              part[(static_cast<long>(z) * p.M + c + i) * p.K + n] = g[i];
+            else
+              out[static_cast<long>(c + i) * p.K + n] = __float2bfloat16_rn(g[i]);
+          }
+        } else {
+          float up[32];
+          tmem_ld32(tacc + 128 + c, up);
+          tmem_ld_wait();
+          if (!valid) continue;
+          __nv_bfloat16 d[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (c + i < p.M) d[i] = du[static_cast<long>(c + i) * p.I + n];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            if (c + i >= p.M) break;
+            float dg, dup;
+            swiglu_grad(g[i], up[i], __bfloat162float(d[i]), &dg, &dup);
+            __nv_bfloat16 *dst = out + static_cast<long>(c + i) * 2 * p.I + n;
+            dst[0] = __float2bfloat16_rn(dg);
+            dst[p.I] = __float2bfloat16_rn(dup);
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&tempty);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tmem_dealloc(tmem_base, TMEM_COLS);
+}
+
+// out[i] = bf16 of the sum of `shares` fp32 partials, in share order; n8 vectors of 8
+__global__ void __launch_bounds__(256)
+    grad_rows_reduce_kernel(const float4 *part, int shares, long n8, uint4 *out) {
+  pdl_wait();
+  pdl_trigger();
+  for (long i = blockIdx.x * static_cast<long>(blockDim.x) + threadIdx.x; i < n8;
+       i += static_cast<long>(gridDim.x) * blockDim.x) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    for (int z = 0; z < shares; ++z) {
+      const float4 p = part[(z * n8 + i) * 2], q = part[(z * n8 + i) * 2 + 1];
+      a.x += p.x; a.y += p.y; a.z += p.z; a.w += p.w;
+      b.x += q.x; b.y += q.y; b.z += q.z; b.w += q.w;
+    }
+    out[i] = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w), pack_bf16x2(b.x, b.y),
+                        pack_bf16x2(b.z, b.w));
+  }
 }
 
 }  // namespace ig4
