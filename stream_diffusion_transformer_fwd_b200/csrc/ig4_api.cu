@@ -92,9 +92,6 @@ ig4_status last_launch_status() {
 // Per-device facts queried once.
 struct DeviceInfo {
   int sms = 0;
-  // clusters of 2, 4, 8 CTAs of the matvec kernels that run at once, with 1 to 3
-  // CTAs on an SM ([gated][fp32 output][size][CTAs]; 0: not asked yet)
-  std::atomic<int> clusters[2][2][3][3] = {};
 };
 constexpr int MAX_DEVICES = 64;
 DeviceInfo g_dev[MAX_DEVICES];
@@ -113,6 +110,8 @@ ig4_status device_info(DeviceInfo **out) {
   *out = &g_dev[dev];
   return IG4_OK;
 }
+
+constexpr size_t DEFAULT_SMEM = 48 << 10;  // dynamic shared memory any kernel may use
 
 // Raise a kernel's dynamic shared-memory limit (idempotent, cheap).
 template <typename K>
@@ -2490,7 +2489,8 @@ ig4_status launch_add_norm_t(int M, int D, const void *x, const void *r, const f
     e = launch_pdl(add_rms_norm_warp_kernel<XT, OUT>, dim3(p.grid), dim3(p.threads), 0, st, xp, rp,
                    g, eps, sp, y, scale, sfp, M, D);
   } else {
-    IG4_TRY(allow_smem(add_rms_norm_kernel<XT, OUT>, static_cast<int>(p.smem)));
+    if (p.smem > DEFAULT_SMEM)
+      IG4_TRY(allow_smem(add_rms_norm_kernel<XT, OUT>, static_cast<int>(p.smem)));
     e = launch_pdl(add_rms_norm_kernel<XT, OUT>, dim3(p.grid), dim3(p.threads), p.smem, st, xp, rp,
                    g, eps, sp, y, scale, sfp, M, D, p.slots);
   }
@@ -2530,7 +2530,8 @@ ig4_status launch_add_norm_grad(int M, int D, const void *s, const float *g, flo
     e = launch_pdl(add_rms_norm_grad_warp_kernel<XT, YT>, dim3(p.grid), dim3(p.threads), 0, st, sp,
                    g, eps, dyp, dsp, dxp, pp, M, D);
   } else {
-    IG4_TRY(allow_smem(add_rms_norm_grad_kernel<XT, YT>, static_cast<int>(p.smem)));
+    if (p.smem > DEFAULT_SMEM)
+      IG4_TRY(allow_smem(add_rms_norm_grad_kernel<XT, YT>, static_cast<int>(p.smem)));
     e = launch_pdl(add_rms_norm_grad_kernel<XT, YT>, dim3(p.grid), dim3(p.threads), p.smem, st, sp,
                    g, eps, dyp, dsp, dxp, pp, M, D, p.slots);
   }
@@ -2598,29 +2599,22 @@ ig4_status launch_rotate_v(const RotateArgs &a, bool adjacent, dim3 grid, cudaSt
   return e == cudaSuccess ? last_launch_status() : IG4_ERR_CUDA;
 }
 
+constexpr int GRAD_SMS = 148;  // sm_100a
+
 // ---- few rows x NVFP4 weights
 
-// Cluster size: the smallest that brings a CTA's share of x under
-// MATVEC_MAX_X_BYTES (then three CTAs, or two, fit an SM), doubled while row
-// tiles leave SMs without a CTA and every warp still has two chunks.
-template <bool DUAL, typename OT>
-ig4_status launch_matvec(int M, int N, int K, const void *x, const MatvecWeights &w0,
-                         const MatvecWeights &w1, const float *bias, void *out, cudaStream_t st) {
+template <int C, bool DUAL, typename OT>
+ig4_status launch_matvec_c(int M, int N, int K, const void *x, const MatvecWeights &w0,
+                           const MatvecWeights &w1, const float *bias, void *out, int cluster,
+                           int warps, cudaStream_t st) {
   DeviceInfo *di = nullptr;
   IG4_TRY(device_info(&di));
-  const int nc = (K + MATVEC_CHUNK - 1) / MATVEC_CHUNK;
-  const int tiles = (N + 127) / 128 * 8;
-  int cluster = 1;
-  auto x_bytes = [&] { return matvec_x_bytes((nc + cluster - 1) / cluster, M); };
-  while (cluster < MATVEC_MAX_CLUSTER && x_bytes() > MATVEC_MAX_X_BYTES) cluster *= 2;
-  while (cluster < MATVEC_MAX_CLUSTER && static_cast<long>(tiles) * cluster < di->sms &&
-         nc >= 4 * cluster * MATVEC_WARPS)
-    cluster *= 2;
-  const int smem = MATVEC_RING_BYTES + x_bytes();
-  auto kern = nvfp4_matvec_kernel<DUAL, OT>;
+  const int smem = matvec_smem(C, warps);
+  auto kern = nvfp4_matvec_kernel<C, DUAL, OT>;
   IG4_TRY(allow_smem(kern, smem));
+  const int tiles = (N + 127) / 128 * 8;
   cudaLaunchConfig_t lc = {};
-  lc.blockDim = dim3(MATVEC_THREADS);
+  lc.blockDim = dim3(32 * warps);
   lc.dynamicSmemBytes = smem;
   lc.stream = st;
   cudaLaunchAttribute attr[2];
@@ -2632,27 +2626,76 @@ ig4_status launch_matvec(int M, int N, int K, const void *x, const MatvecWeights
   attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = cluster > 1 ? 2 : 1;
-  // Row tiles are dealt out in advance, so all CTAs have to run at once.  With
-  // clusters the device holds fewer than its SMs suggest (a cluster stays in one
-  // GPC); how many, for so many CTAs on an SM, is asked once.
-  const int per_sm = std::min(MATVEC_CTAS, MATVEC_SM_SMEM / (smem + MATVEC_STATIC_SMEM));
-  int most = per_sm * di->sms;
-  if (cluster > 1) {
-    const int lg = cluster == 2 ? 0 : cluster == 4 ? 1 : 2;
-    std::atomic<int> &known = di->clusters[DUAL ? 1 : 0][sizeof(OT) == 4][lg][per_sm - 1];
-    most = known.load(std::memory_order_relaxed);
-    if (most == 0) {
-      lc.gridDim = dim3(di->sms / cluster * cluster);
-      if (cudaOccupancyMaxActiveClusters(&most, kern, &lc) != cudaSuccess || most < 1)
+  // Row tiles are dealt out in advance, so all clusters have to run at once:
+  // as many as the device holds (fewer than its SMs would suggest where a
+  // cluster does not fit the rest of a GPC), a fact of kernel and device.
+  static std::atomic<int> fit[MAX_DEVICES][4][MATVEC_MAX_WARPS + 1];
+  const int lg = cluster == 1 ? 0 : cluster == 2 ? 1 : cluster == 4 ? 2 : 3;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return IG4_ERR_CUDA;
+  std::atomic<int> &known = fit[dev][lg][warps];
+  int most = known.load(std::memory_order_relaxed);
+  if (most == 0) {
+    if (cluster == 1) {
+      int per_sm = 0;
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 32 * warps, smem) !=
+          cudaSuccess)
         return IG4_ERR_CUDA;
-      known.store(most, std::memory_order_relaxed);
+      most = per_sm * di->sms;
+    } else {
+      lc.gridDim = dim3(2 * di->sms / cluster * cluster);
+      if (cudaOccupancyMaxActiveClusters(&most, kern, &lc) != cudaSuccess) return IG4_ERR_CUDA;
     }
+    if (most < 1) return IG4_ERR_CUDA;
+    known.store(most, std::memory_order_relaxed);
   }
   lc.gridDim = dim3(std::min(tiles, most) * cluster);
   if (cudaLaunchKernelEx(&lc, kern, static_cast<const __nv_bfloat16 *>(x), w0, w1, bias,
                          static_cast<OT *>(out), M, N, K, tiles, cluster) != cudaSuccess)
     return IG4_ERR_CUDA;
   return last_launch_status();
+}
+
+// Warps of a CTA and CTAs of a cluster.  The clusters that run at once take the
+// row tiles in rounds, and a round lasts as long as its SM's warps need for their
+// chunks: the choice with the least rounds x chunks x warps on an SM, at least 12
+// of them counted (fewer do not hide their latency).  Full width: 12 warps and no
+// cluster for K = 4608 (4608 rows: 6.5 us, 7.7 with 8 warps in clusters of 2; the
+// gated pair 26.6 and 27.7), 16 warps in clusters of 2 for K = 12288 (13.1 us, 13.6
+// with 8 in clusters of 4, of which 71 fit and 72 would have to).
+struct MatvecPlan {
+  int warps, cluster, chunks;
+};
+MatvecPlan matvec_plan(int nc, long tiles) {
+  MatvecPlan best{};
+  long best_cost = 0;
+  for (int cl = 1; cl <= MATVEC_MAX_CLUSTER; cl *= 2) {
+    for (int w = MATVEC_MIN_WARPS; w <= MATVEC_MAX_WARPS; ++w) {
+      const int chunks = (nc + cl * w - 1) / (cl * w);
+      if (chunks > MATVEC_MAX_CHUNKS) continue;
+      const int per_sm = w == MATVEC_MIN_WARPS ? 2 : 1;
+      // (clusters of 4 and 8 do not fill every GPC)
+      const long at_once = std::max(1, per_sm * (cl <= 2 ? GRAD_SMS : cl == 4 ? 142 : 128) / cl);
+      const long cost = (tiles + at_once - 1) / at_once * chunks * std::max(12, per_sm * w);
+      if (best.warps == 0 || cost < best_cost) {
+        best = {w, cl, chunks};
+        best_cost = cost;
+      }
+    }
+  }
+  return best;
+}
+
+template <bool DUAL, typename OT>
+ig4_status launch_matvec(int M, int N, int K, const void *x, const MatvecWeights &w0,
+                         const MatvecWeights &w1, const float *bias, void *out, cudaStream_t st) {
+  const int nc = (K + MATVEC_CHUNK - 1) / MATVEC_CHUNK;
+  const MatvecPlan p = matvec_plan(nc, (N + 127L) / 128 * 8);
+  switch (p.chunks) {
+    case 1: return launch_matvec_c<1, DUAL, OT>(M, N, K, x, w0, w1, bias, out, p.cluster, p.warps, st);
+    case 2: return launch_matvec_c<2, DUAL, OT>(M, N, K, x, w0, w1, bias, out, p.cluster, p.warps, st);
+    default: return launch_matvec_c<3, DUAL, OT>(M, N, K, x, w0, w1, bias, out, p.cluster, p.warps, st);
+  }
 }
 
 bool matvec_args_ok(int M, int N, int K, const void *x, const MatvecWeights *w, int n_w,
@@ -2726,7 +2769,6 @@ GradPlan swiglu_dh_plan(int M, int I, int K) {
 }
 
 // Up to 128 tokens: the plans of G^T, U^T and of dh^T (see GradRowsPlan).
-constexpr int GRAD_SMS = 148;
 constexpr int GRAD_ROWS_MAX_M = 128;
 GradRowsPlan grad_rows_plan(bool dh, int M, int I, int K) {
   GradRowsPlan p{};
