@@ -2458,7 +2458,7 @@ AddNormPlan addnorm_plan(int M, int D, size_t slot_bytes, int sms, int threads_p
   p.warp = D <= ADDNORM_WARP_D;
   const int nvec = D / 8;
   p.threads = p.warp ? 32 * ADDNORM_WARPS : 32 * ((nvec + 32 * ADDNORM_NV - 1) / (32 * ADDNORM_NV));
-  int ctas = std::max(1, std::min(threads_per_sm, p.warp ? 512 : 2048) / p.threads);
+  int ctas = std::max(1, threads_per_sm / p.threads);
   if (!p.warp) {
     while (ctas > 1 && ctas * (addnorm_smem(slot_bytes, 2) + 1024) > ADDNORM_SM_SMEM) --ctas;
     p.slots = 2;
@@ -2471,6 +2471,11 @@ AddNormPlan addnorm_plan(int M, int D, size_t slot_bytes, int sms, int threads_p
   p.slots = static_cast<int>(std::min<long>(p.slots, (rows + p.grid - 1) / p.grid));
   p.smem = addnorm_smem(slot_bytes, p.slots);
   return p;
+}
+// (a warp of the gradients' warp-per-row form takes 128 to 165 registers a thread)
+AddNormPlan addnorm_grad_plan(int M, int D, size_t slot_bytes, int sms) {
+  return addnorm_plan(M, D, slot_bytes, sms,
+                      D <= ADDNORM_WARP_D ? 512 : ADDNORM_BWD_THREADS_PER_SM);
 }
 constexpr int ADDNORM_MAX_SMS = 160;  // bounds the partial rows of dg in the workspace
 
@@ -2519,8 +2524,7 @@ ig4_status launch_add_norm_grad(int M, int D, const void *s, const float *g, flo
   DeviceInfo *di = nullptr;
   IG4_TRY(device_info(&di));
   const size_t slot = static_cast<size_t>(D) * ((ds ? 2 : 1) * sizeof(XT) + sizeof(YT));
-  const AddNormPlan p = addnorm_plan(M, D, slot, std::min(di->sms, ADDNORM_MAX_SMS),
-                                     ADDNORM_BWD_THREADS_PER_SM);
+  const AddNormPlan p = addnorm_grad_plan(M, D, slot, std::min(di->sms, ADDNORM_MAX_SMS));
   float *pp = dg ? part : nullptr;
   const XT *sp = static_cast<const XT *>(s), *dsp = static_cast<const XT *>(ds);
   const YT *dyp = static_cast<const YT *>(dy);
@@ -2922,7 +2926,7 @@ ig4_status ig4_add_rms_norm(int M, int D, const void *x, const void *r, int x_dt
 size_t ig4_add_rms_norm_backward_workspace_size(int M, int D) {
   if (!addnorm_sizes_ok(M, D)) return 0;
   // the smallest slots allow the most CTAs
-  const AddNormPlan p = addnorm_plan(M, D, 4ul * D, ADDNORM_MAX_SMS, ADDNORM_BWD_THREADS_PER_SM);
+  const AddNormPlan p = addnorm_grad_plan(M, D, 4ul * D, ADDNORM_MAX_SMS);
   return round_up(static_cast<size_t>(p.grid) * D * 4, 256);
 }
 
