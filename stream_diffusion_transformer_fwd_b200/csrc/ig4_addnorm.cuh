@@ -98,6 +98,16 @@ __device__ __forceinline__ float max8(const uint64_t (&v)[4], float m) {
 }
 __device__ __forceinline__ float sum2(uint64_t v) { return f2_lo(v) + f2_hi(v); }
 
+// 1 / sqrt(v) to half a step: rsqrtf (2 steps) and one Newton correction with the
+// residual 1 - v r^2 in two parts.  An error here is common to a whole row, and
+// moves that many more of its values across a rounding border.
+__device__ __forceinline__ float norm_rsqrt(float v) {
+  const float r = rsqrtf(v);
+  const float t = v * r;
+  const float e = fmaf(-fmaf(v, r, -t), r, fmaf(-t, r, 1.0f));
+  return v < INFINITY ? fmaf(0.5f * r, e, r) : r;
+}
+
 // Weight of vector vi (1 without a weight)
 __device__ __forceinline__ void load_g8(const float *g, int vi, uint64_t (&v)[4]) {
   Raw8<float> w;
@@ -212,7 +222,7 @@ __global__ void __launch_bounds__(32 * ADDNORM_WARPS)
       cx[i] = nx[i];
       cr[i] = nr[i];
     }
-    const float rstd = rsqrtf(fmaf(warp_sum(sum2(ss)), inv_d, eps));
+    const float rstd = norm_rsqrt(fmaf(warp_sum(sum2(ss)), inv_d, eps));
     const uint64_t rstd2 = f2_pack(rstd, rstd);
     float amax = 0.0f;
 #pragma unroll
@@ -318,7 +328,7 @@ __global__ void __launch_bounds__(32 * ADDNORM_WARPS)
       cy[i].get(b);
       grad_sums(a, b, gv[i], ss, dot);
     }
-    const float rstd = rsqrtf(fmaf(warp_sum(sum2(ss)), inv_d, eps));
+    const float rstd = norm_rsqrt(fmaf(warp_sum(sum2(ss)), inv_d, eps));
     const float negm = -warp_sum(sum2(dot)) * rstd * inv_d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -457,7 +467,7 @@ __global__ void __launch_bounds__(ADDNORM_MAX_THREADS)
     cta_put(warp_sum(sum2(ss)), rd);
     __syncthreads();
     if (tid == 0) issue();  // every thread has read its part of the slot
-    const float rstd = rsqrtf(fmaf(cta_sum(rd, quads), inv_d, eps));
+    const float rstd = norm_rsqrt(fmaf(cta_sum(rd, quads), inv_d, eps));
     const uint64_t rstd2 = f2_pack(rstd, rstd);
     float amax = 0.0f;
 #pragma unroll
@@ -552,7 +562,7 @@ __global__ void __launch_bounds__(ADDNORM_BWD_THREADS_PER_SM)
     cta_put(warp_sum(sum2(dot)), rd + 16);
     __syncthreads();
     if (tid == 0) issue();  // every thread has read its part of the slot
-    const float rstd = rsqrtf(fmaf(cta_sum(rd, quads), inv_d, eps));
+    const float rstd = norm_rsqrt(fmaf(cta_sum(rd, quads), inv_d, eps));
     const float negm = -cta_sum(rd + 16, quads) * rstd * inv_d;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
