@@ -255,13 +255,14 @@ size_t ig4_mx8_scale_bytes(int M, int K);
  * per row, in fp32; the norm takes the unrounded sum t.  x, r, s_out [M][D] in
  * x_dtype (F32 or BF16); r NULL: t = x; g fp32 [D], NULL: all ones; s_out NULL:
  * not wanted.  y_out [M][D] in y_dtype: F32, BF16, or E4M3 with exactly one of
- *   y_scale_out  fp32 [M]: scale[m] = max|y[m]| / 448 (1 for a zero row), codes
- *                of y / scale, as ig4_quantize_rows;
+ *   y_scale_out  fp32 [M]: scale[m] = max|y[m]| / 448, at least 2^-126 (1 for a
+ *                zero row), codes of y / scale, as ig4_quantize_rows;
  *   y_sf_out     ig4_mx8_scale_bytes(M, D) bytes: the MX8 form of
  *                ig4_quantize_mx8 of the bf16-rounded y (padding rows are not
  *                written); D % 128 == 0.
- * A row that holds an infinity or a NaN comes out as NaN where y is NaN.
- * M >= 1, D % 8 == 0, D <= 8192, eps > 0.  s_out may be x or r; otherwise the
+ * A row that holds an infinity or a NaN comes out as NaN where y is NaN.  Squares
+ * are summed in fp32: |t| up to 2^57 (where a sum overflows, its row of y is 0).
+ * M >= 1, D % 8 == 0, D <= 8192, eps > 0 and finite.  s_out may be x or r; otherwise the
  * outputs overlap neither an input nor one another.  Matrices and g 16-byte
  * aligned, y_scale_out and y_sf_out 4-byte.  Errors: INVALID_ARG. */
 ig4_status ig4_add_rms_norm(int M, int D, const void *x, const void *r, int x_dtype,
@@ -321,8 +322,10 @@ typedef struct ig4_heads {
  * ig4_mrope_positions writes it).  Any alignment of the element type and any
  * strides are taken; rows whose pointers and strides are 16-byte multiples
  * move fastest.  An output is its own input (same pointer and strides: in
- * place) or overlaps no input; no two elements of an output coincide.
- * B, L, H >= 1, B * L < 2^31.  Errors: INVALID_ARG. */
+ * place) or shares no element with an input (views of one buffer may
+ * interleave), and no two elements of the outputs coincide; pos lies outside
+ * the outputs.  B, L, H >= 1, B * L < 2^31.  Errors: INVALID_ARG, for views whose
+ * strides nest in no order and whose extents overlap too. */
 ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long pos_stride_b,
                             const ig4_heads *q, const ig4_heads *q_out, const ig4_heads *k,
                             const ig4_heads *k_out, void *stream);

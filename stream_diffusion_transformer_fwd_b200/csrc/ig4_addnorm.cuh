@@ -163,9 +163,10 @@ __device__ __forceinline__ void store_mx8(const uint64_t (&t)[4], bool in, int v
   }
 }
 
-// scale = max|y| / 448 (1 for a zero row), codes of the fp32 y
+// scale = max|y| / 448 (1 for a zero row), codes of the fp32 y; at least 2^-126, whose
+// reciprocal is finite
 __device__ __forceinline__ float row8_scale(float amax) {
-  return amax > 0.0f ? amax / 448.0f : 1.0f;
+  return amax > 0.0f ? fmaxf(amax / 448.0f, 0x1p-126f) : 1.0f;
 }
 
 template <int OUT>

@@ -232,8 +232,10 @@ ig4_status launch_gemm(const CUtensorMap &A, const CUtensorMap &B, const CUtenso
       return last_launch_status();
     }
   }
-  if constexpr (BN == 240) {
-    return IG4_ERR_UNSUPPORTED;  // 240-wide tiles run on CTA pairs only
+  if constexpr (BN == 240 || std::is_same<Epi, EpiSwiGLUGrad>::value) {
+    // 240-wide tiles run on CTA pairs only; the SwiGLU gradients of up to
+    // GEMM_BM tokens do not come here
+    return IG4_ERR_UNSUPPORTED;
   } else {
   auto kern = gemm_tc_kernel<BN, FP8, DUAL_B, Epi>;
   constexpr int SMEM = GemmShape<BN>::SMEM_BYTES;
@@ -2565,11 +2567,67 @@ bool heads_distinct(const ig4_heads &t, int B, int L, int d) {
   }
   return true;
 }
-bool heads_ok(const ig4_heads &t, int esize) {
-  constexpr long long MAX_STRIDE = 1LL << 40;
-  return t.data && t.H >= 1 && t.H <= (1 << 20) && t.stride_b >= 0 && t.stride_l >= 0 &&
-         t.stride_h >= 0 && t.stride_b < MAX_STRIDE && t.stride_l < MAX_STRIDE &&
-         t.stride_h < MAX_STRIDE && reinterpret_cast<uintptr_t>(t.data) % esize == 0;
+bool heads_ok(const ig4_heads &t, int B, int L, int esize) {
+  constexpr long long MAX_STRIDE = 1LL << 40, MAX_EXTENT = 1LL << 52;  // no sum below overflows
+  const auto fits = [](long long s, int n) {
+    return s >= 0 && s < MAX_STRIDE && s <= MAX_EXTENT / std::max(1, n - 1);
+  };
+  return t.data && t.H >= 1 && t.H <= (1 << 20) && fits(t.stride_b, B) && fits(t.stride_l, L) &&
+         fits(t.stride_h, t.H) && reinterpret_cast<uintptr_t>(t.data) % esize == 0;
+}
+// First and last element of the tensor, as an extent past its data
+long long heads_extent(const ig4_heads &t, int B, int L, int d) {
+  return (B - 1) * t.stride_b + (L - 1) * t.stride_l + (t.H - 1) * t.stride_h + d;
+}
+
+// Whether two tensors of heads share an element: whether some sum of their
+// strides' multiples, the steps of x less those of y, makes up the distance of
+// their first elements.  Views of one buffer interleave (q and k of a fused
+// projection), so extents alone cannot tell.  The largest stride is tried
+// first; what the smaller ones can still reach leaves one or two multiples of
+// it for nested views.  Strides that nest in no order may leave many: past
+// HEADS_SEARCH of them the answer is yes.
+struct HeadsTerm {
+  long long s, lo, hi;            // stride, least and largest multiple
+  long long rest_lo, rest_hi;     // what the terms behind it can add
+};
+constexpr int HEADS_SEARCH = 4096;
+bool heads_reach(const HeadsTerm *t, int n, long long dist, int *budget) {
+  const long long lo = t->s * t->lo + t->rest_lo, hi = t->s * t->hi + t->rest_hi;
+  if (dist < lo || dist > hi) return false;
+  if (n == 1) return true;  // the elements of a head, one apart
+  const auto floor_div = [](long long a, long long b) { return a >= 0 ? a / b : -((-a + b - 1) / b); };
+  const long long first = std::max(t->lo, -floor_div(-(dist - t->rest_hi), t->s));
+  const long long last = std::min(t->hi, floor_div(dist - t->rest_lo, t->s));
+  for (long long m = first; m <= last; ++m)
+    if (--*budget <= 0 || heads_reach(t + 1, n - 1, dist - m * t->s, budget)) return true;
+  return false;
+}
+bool heads_meet(const ig4_heads &x, const ig4_heads &y, int B, int L, int d, int esize) {
+  const long long dist =
+      (reinterpret_cast<intptr_t>(y.data) - reinterpret_cast<intptr_t>(x.data)) / esize;
+  if (dist >= heads_extent(x, B, L, d) || -dist >= heads_extent(y, B, L, d)) return false;
+  const long long sx[3] = {x.stride_b, x.stride_l, x.stride_h};
+  const long long sy[3] = {y.stride_b, y.stride_l, y.stride_h};
+  const int nx[3] = {B, L, x.H}, ny[3] = {B, L, y.H};
+  HeadsTerm t[7];
+  int n = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (sx[i] == sy[i] && sx[i] > 0) {
+      t[n++] = {sx[i], 1LL - ny[i], nx[i] - 1LL, 0, 0};
+    } else {
+      if (sx[i] > 0 && nx[i] > 1) t[n++] = {sx[i], 0, nx[i] - 1LL, 0, 0};
+      if (sy[i] > 0 && ny[i] > 1) t[n++] = {sy[i], 1LL - ny[i], 0, 0, 0};
+    }
+  }
+  std::sort(t, t + n, [](const HeadsTerm &a, const HeadsTerm &b) { return a.s > b.s; });
+  t[n++] = {1, 1LL - d, d - 1LL, 0, 0};
+  for (int i = n - 2; i >= 0; --i) {
+    t[i].rest_lo = t[i + 1].rest_lo + t[i + 1].s * t[i + 1].lo;
+    t[i].rest_hi = t[i + 1].rest_hi + t[i + 1].s * t[i + 1].hi;
+  }
+  int budget = HEADS_SEARCH;
+  return heads_reach(t, n, dist, &budget);
 }
 bool heads_vec(const ig4_heads &t, int V, int esize) {
   return reinterpret_cast<uintptr_t>(t.data) % (V * esize) == 0 && t.stride_b % V == 0 &&
@@ -2897,7 +2955,8 @@ extern "C" {
 ig4_status ig4_add_rms_norm(int M, int D, const void *x, const void *r, int x_dtype,
                             const float *g, float eps, void *s_out, void *y_out, int y_dtype,
                             float *y_scale_out, void *y_sf_out, void *stream) {
-  if (!addnorm_sizes_ok(M, D) || !x || !y_out || !(eps > 0.0f)) return IG4_ERR_INVALID_ARG;
+  if (!addnorm_sizes_ok(M, D) || !x || !y_out || !(eps > 0.0f) || std::isinf(eps))
+    return IG4_ERR_INVALID_ARG;
   if (!valid_dtype_x(x_dtype) || (!valid_dtype_x(y_dtype) && y_dtype != IG4_E4M3))
     return IG4_ERR_INVALID_ARG;
   const bool f8 = y_dtype == IG4_E4M3;
@@ -2934,7 +2993,8 @@ ig4_status ig4_add_rms_norm_backward(int M, int D, const void *s, int s_dtype, c
                                      float eps, const void *dy, int dy_dtype, const void *ds,
                                      void *dx_out, float *dg_out, void *workspace,
                                      size_t ws_bytes, void *stream) {
-  if (!addnorm_sizes_ok(M, D) || !s || !dy || !dx_out || !(eps > 0.0f)) return IG4_ERR_INVALID_ARG;
+  if (!addnorm_sizes_ok(M, D) || !s || !dy || !dx_out || !(eps > 0.0f) || std::isinf(eps))
+    return IG4_ERR_INVALID_ARG;
   if (!valid_dtype_x(s_dtype) || !valid_dtype_x(dy_dtype)) return IG4_ERR_INVALID_ARG;
   if (!aligned16(s) || !aligned16(g) || !aligned16(dy) || !aligned16(ds) || !aligned16(dx_out) ||
       reinterpret_cast<uintptr_t>(dg_out) % 4)
@@ -2989,7 +3049,8 @@ ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long
   for (int w = 0; w < 2; ++w) {
     if (!ins[w]) continue;
     const ig4_heads &i = *ins[w], &o = *outs[w];
-    if (!heads_ok(i, es) || !heads_ok(o, es) || i.H != o.H || !heads_distinct(o, B, L, d))
+    if (!heads_ok(i, B, L, es) || !heads_ok(o, B, L, es) || i.H != o.H ||
+        !heads_distinct(o, B, L, d))
       return IG4_ERR_INVALID_ARG;
     if (i.data == o.data &&
         (i.stride_b != o.stride_b || i.stride_l != o.stride_l || i.stride_h != o.stride_h))
@@ -2999,7 +3060,17 @@ ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long
               o.stride_b, o.stride_l, o.stride_h, {}, {}};
     heads += i.H;
   }
-  if (k_out && k_out->data == q_out->data) return IG4_ERR_INVALID_ARG;
+  const Span table{pos, ((B - 1) * static_cast<size_t>(pos_stride_b) + 3ul * L) * 4};
+  for (int o = 0; o < 2; ++o) {
+    if (!outs[o]) continue;
+    const size_t extent = heads_extent(*outs[o], B, L, d);
+    if (overlap(table, {outs[o]->data, extent * es})) return IG4_ERR_INVALID_ARG;
+    for (int i = 0; i < 2; ++i)  // (in place: same pointer and strides, checked above)
+      if (ins[i] && !(i == o && ins[i]->data == outs[o]->data) &&
+          heads_meet(*ins[i], *outs[o], B, L, d, es))
+        return IG4_ERR_INVALID_ARG;
+  }
+  if (k_out && heads_meet(*q_out, *k_out, B, L, d, es)) return IG4_ERR_INVALID_ARG;
   for (int j = 0, turn = 0; j < R / 2; ++j) {
     if (!rot->interleaved) turn = 0;
     while (left[turn] == 0) turn = (turn + 1) % 3;

@@ -561,6 +561,7 @@ def ig4_denoise_step(cfg: Config, cond: StackWeights, uncond: StackWeights, z, t
 
 _FLOATS = (torch.float32, torch.bfloat16)
 _OUTPUTS = _FLOATS + (torch.float8_e4m3fn,)
+_INT_MAX = 2 ** 31 - 1  # ctypes cuts larger integers off without a word
 
 
 def ig4_add_rms_norm(x, r, g, eps, s_out, y_out, y_scale_out=None, y_sf_out=None, stream=None):
@@ -574,6 +575,8 @@ def ig4_add_rms_norm(x, r, g, eps, s_out, y_out, y_scale_out=None, y_sf_out=None
         _refuse(name)
     D = shape[-1]
     M = n // D
+    if M > _INT_MAX:
+        _refuse(name)
     if y_sf_out is not None and y_sf_out.numel() < ig4_mx8_scale_bytes(M, D):
         _refuse(name)
     _check(_lib.ig4_add_rms_norm(
@@ -598,9 +601,12 @@ def ig4_add_rms_norm_backward(s, g, eps, dy, ds, dx_out, dg_out, workspace=None,
     if n == 0 or not shape:
         _refuse(name)
     D = shape[-1]
+    M = n // D
+    if M > _INT_MAX:
+        _refuse(name)
     ws, ws_bytes = _scratch(name, dev, workspace)
     _check(_lib.ig4_add_rms_norm_backward(
-        n // D, D, _dense(name, dev, s, shape, *_FLOATS), _DTYPE_CODE[dt],
+        M, D, _dense(name, dev, s, shape, *_FLOATS), _DTYPE_CODE[dt],
         _dense(name, dev, g, (D,), torch.float32), eps, _dense(name, dev, dy, shape, *_FLOATS),
         _DTYPE_CODE[dy.dtype], _dense(name, dev, ds, shape, dt),
         _dense(name, dev, dx_out, shape, dt), _dense(name, dev, dg_out, (D,), torch.float32),

@@ -200,3 +200,50 @@ def test_binding_refuses_host_tensors(ig4):
         with pytest.raises(ig4.Ig4Error) as e:
             call()
         assert e.value.status == ig4.IG4_ERR_INVALID_ARG
+
+
+# ------------------------------------------------- outputs on other operands
+
+PACKED = 10 * 256                                        # a row of 10 heads: q 0-3, k 4-5, v 6-9
+
+
+def packed(buffer, head, H, l=PACKED):
+    return at(buffer, head * 512), H, 16 * l, l, 256
+
+
+@pytest.mark.parametrize("bad", [
+    dict(q=packed(0, 0, 4), qo=packed(0, 2, 4)),         # its own heads, shifted by two
+    dict(q=packed(0, 0, 4), qo=packed(0, 0, 4)[:1] + (4, 16 * 1024, 1024, 256)),
+    dict(q=packed(0, 0, 4), qo=packed(0, 10, 4)),        # shifted by a token
+    dict(q=packed(0, 0, 4), qo=(at(0, 20 * 256 * 15), 4, 16 * 1024, 1024, 256)),
+    dict(q=packed(0, 0, 4), qo=packed(1, 0, 4), k=packed(0, 4, 2), ko=packed(0, 3, 2)),
+    dict(q=packed(0, 0, 4), qo=packed(1, 0, 4), k=packed(0, 4, 2), ko=packed(1, 3, 2)),
+    dict(q=packed(0, 0, 4), qo=packed(0, 4, 4), k=packed(0, 4, 2), ko=packed(1, 0, 2)),
+    dict(qo=(at(9, -4 * 1024), 4, 16 * 1024, 1024, 256)),             # the positions
+    dict(q=(at(0), 4, 1 << 39, 1 << 39, 1 << 39), B=1 << 15, L=1 << 15)])
+def test_mrope_rotate_refuses_outputs_on_other_operands(ig4, bad):
+    assert rotate(ig4, **bad) == ig4.IG4_ERR_INVALID_ARG
+
+
+def test_norms_refuse_an_infinite_eps(ig4):
+    for call in (norm, grad):
+        assert call(ig4, eps=float("inf")) == ig4.IG4_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("rows", [2 ** 31, 2 ** 32 + 4])
+def test_binding_refuses_more_rows_than_an_int(ig4, monkeypatch, rows):
+    class Rows:
+        is_cuda, shape, dtype = True, (rows, 8), torch.bfloat16
+        get_device, numel, is_contiguous, data_ptr = (
+            lambda s: 0, lambda s: rows * 8, lambda s: True, lambda s: 1 << 44)
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(ig4, "_stream_on", lambda dev, stream: 0)
+    monkeypatch.setattr(ig4._lib, "ig4_add_rms_norm", None)   # the library is not reached
+    monkeypatch.setattr(ig4._lib, "ig4_add_rms_norm_backward", None)
+    x = Rows()
+    for call in (lambda: ig4.ig4_add_rms_norm(x, None, None, 1e-6, None, x),
+                 lambda: ig4.ig4_add_rms_norm_backward(x, None, 1e-6, x, None, x, None)):
+        with pytest.raises(ig4.Ig4Error) as e:
+            call()
+        assert e.value.status == ig4.IG4_ERR_INVALID_ARG

@@ -268,3 +268,76 @@ def test_capture_and_another_stream(ig4):
     graph.replay()
     done(ig4)
     assert all(torch.equal(a, b) for a, b in zip(want, (s, y, dx, dg)))
+
+
+@pytest.mark.parametrize("D", [128, 1280])
+def test_tiny_rows_keep_finite_codes(ig4, D):
+    """Rows so small that max|y| / 448 has no finite reciprocal: codes of y / 2^-126, half a step
+    of E4M3's smallest numbers (2^-10) off at most, and zeros stay zeros."""
+    x = torch.zeros(5, D, device="cuda")
+    x[1, ::3], x[2, 7], x[3, ::2], x[4, 5] = 1e-40, -1e-42, 3e-38, 2.0 ** -120
+    y = torch.empty(5, D, dtype=torch.float8_e4m3fn, device="cuda")
+    scale = torch.empty(5, device="cuda")
+    ig4.ig4_add_rms_norm(x, None, None, 1.0, None, y, y_scale_out=scale)
+    done(ig4)
+    amax = x.double().abs().amax(-1)
+    least = torch.where(amax > 0, (amax / 448).clamp(min=2.0 ** -126), 1.0)
+    assert torch.all((scale.double() - least).abs() <= 2.0 ** -23 * least)
+    got = y.double() * scale.double()[:, None]
+    # eps / 2 of the code, half its smallest step, and the fp32 subnormals of y itself
+    tol = (2.0 ** -4 + 2.0 ** -20) * x.double().abs() + 2.0 ** -10 * scale.double()[:, None] + 2.0 ** -149
+    assert torch.all((got - x.double()).abs() <= tol)
+
+
+@pytest.mark.parametrize("D", [256, 1280])
+def test_rows_whose_squares_overflow(ig4, D):
+    """|t| up to 2^57 is exact as any; a row whose squares overflow comes out as zero."""
+    x = torch.randn(3, D, device="cuda")
+    x[0] *= 2.0 ** 54
+    x[1] *= 2.0 ** 70
+    y = torch.empty_like(x)
+    ig4.ig4_add_rms_norm(x, None, None, 1e-6, None, y)
+    done(ig4)
+    _, y64 = reference(x, None, None, 1e-6)
+    assert torch.all((y[::2].double() - y64[::2]).abs() <= (half(y.dtype) + C32) * y64[::2].abs())
+    assert torch.all(y[1] == 0)
+
+
+def test_offsets_past_32_bits(ig4):
+    """More than 2^31 elements: the last rows come out as those rows alone."""
+    D = 512
+    M = (1 << 31) // D + 700
+    x = torch.zeros(M, D, dtype=torch.bfloat16, device="cuda")
+    x[-300:] = torch.randn(300, D, device="cuda").to(x.dtype)
+    y, tail = torch.empty_like(x), torch.empty_like(x[-300:])
+    ig4.ig4_add_rms_norm(x, None, None, 1e-6, None, y)
+    ig4.ig4_add_rms_norm(x[-300:], None, None, 1e-6, None, tail)
+    done(ig4)
+    assert torch.equal(y[-300:], tail) and not y[:300].any()
+
+
+def test_binding_refuses(ig4):
+    x, g = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda"), torch.ones(256, device="cuda")
+    y, f8 = torch.empty_like(x), torch.empty(4, 256, dtype=torch.float8_e4m3fn, device="cuda")
+    sc, dg = torch.empty(4, device="cuda"), torch.empty(256, device="cuda")
+    sf = torch.empty(64, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    forward = [(x[:0], None, g, 1e-6, None, y[:0]), (x, x[:2], g, 1e-6, None, y),
+               (x, x.float(), g, 1e-6, None, y), (x, None, g.bfloat16(), 1e-6, None, y),
+               (x, None, g[:128], 1e-6, None, y), (x, None, g, 1e-6, y.float(), y),
+               (x.half(), None, g, 1e-6, None, y), (x, None, g, 1e-6, None, y.half()),
+               (x, None, g, 1e-6, None, y.t().contiguous().t()), (x[:, :200], None, None, 1e-6, None, y),
+               (x, None, g, 1e-6, None, f8, sc[:2]), (x, None, g, 1e-6, None, f8, None, sf),
+               (x, None, g, 1e-6, None, f8, sc, sf), (x, None, g.cpu(), 1e-6, None, y)]
+    backward = [(x, g, 1e-6, x[:2], None, y, dg, ws), (x, g, 1e-6, x.half(), None, y, dg, ws),
+                (x, g, 1e-6, x, x.float(), y, dg, ws), (x, g, 1e-6, x, None, y.float(), dg, ws),
+                (x, g, 1e-6, x, None, y, dg.bfloat16(), ws), (x, g, 1e-6, x, None, x, dg, ws),
+                (x, g, 1e-6, x, None, y, dg, ws.cpu())]
+    for call, cases in ((ig4.ig4_add_rms_norm, forward), (ig4.ig4_add_rms_norm_backward, backward)):
+        for args in cases:
+            with pytest.raises(ig4.Ig4Error) as e:
+                call(*args)
+            assert e.value.status == ig4.IG4_ERR_INVALID_ARG
+    with pytest.raises(ig4.Ig4Error) as e:
+        ig4.ig4_add_rms_norm_backward(x, g, 1e-6, x, None, y, dg, ws[:256])
+    assert e.value.status == ig4.IG4_ERR_WORKSPACE

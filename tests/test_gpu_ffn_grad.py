@@ -142,3 +142,21 @@ def test_same_bits_again_captured_and_on_another_stream(ig4):
     torch.cuda.synchronize()
     assert ig4.ig4_last_device_error() == ig4.IG4_OK
     assert all(torch.equal(a, b) for a, b in zip(want, out))
+
+
+def test_binding_refuses(ig4):
+    h, wg, wu, du = make(8, 256, 128)
+    ws = torch.empty(ig4.ig4_swiglu_backward_workspace_size(8, 256, 128), dtype=torch.uint8,
+                     device="cuda")
+    dh, dg, du_w = torch.empty_like(h), torch.empty_like(wg), torch.empty_like(wu)
+    good = [h, wg, wu, du, dh, dg, du_w, ws]
+    for i, bad in ((0, h.float()), (0, h[:, :64]), (1, wg[:128]), (2, wu.t()), (2, wu.half()),
+                   (3, du[:4]), (3, du.float()), (4, dh[:, ::2]), (4, h), (5, dg.float()), (5, None),
+                   (6, du_w.cpu()), (6, dg), (7, ws[::2])):
+        with pytest.raises(ig4.Ig4Error) as e:
+            ig4.ig4_swiglu_backward(*good[:i], bad, *good[i + 1:])
+        assert e.value.status == ig4.IG4_ERR_INVALID_ARG
+    for bad in (None, ws[:-1]):
+        with pytest.raises(ig4.Ig4Error) as e:
+            ig4.ig4_swiglu_backward(*good[:7], bad)
+        assert e.value.status == ig4.IG4_ERR_WORKSPACE

@@ -189,3 +189,38 @@ def test_capture_and_another_stream(ig4):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_views_of_one_buffer_interleave(ig4):
+    """q into the place of another part of the same rows, k in place beside it."""
+    B, L, d = 2, 33, 256
+    buf = make(11, "blhd", B, L, 10, d, torch.bfloat16)
+    before = buf.clone()
+    pos = torch.randint(0, 99, (3, L), dtype=torch.int32, device="cuda")
+    q, k, qo = buf[:, :, :4], buf[:, :, 4:6], buf[:, :, 6:]
+    ig4.ig4_mrope_rotate(q, k, pos, 5e6, (24, 20, 20), qo, k)
+    torch.cuda.synchronize()
+    check(qo, before[:, :, :4], pos, 5e6, (24, 20, 20), False, False, False)
+    check(k, before[:, :, 4:6], pos, 5e6, (24, 20, 20), False, False, False)
+    assert torch.equal(q, before[:, :, :4])
+
+
+def test_binding_refuses(ig4):
+    q = make(12, "blhd", 2, 5, 3, 256, torch.bfloat16)
+    out, pos = torch.empty_like(q), torch.zeros(3, 5, dtype=torch.int32, device="cuda")
+    sec = (24, 20, 20)
+    for args in ((q[0], None, pos, 5e6, sec, out[0], None),
+                 (q, None, pos.long(), 5e6, sec, out, None),
+                 (q, None, pos[:, :4], 5e6, sec, out, None),
+                 (q, None, pos.cpu(), 5e6, sec, out, None),
+                 (q, None, pos.t().contiguous().t(), 5e6, sec, out, None),
+                 (q, None, pos, 5e6, sec, out.float(), None),
+                 (q, None, pos, 5e6, sec, out[:, :4], None),
+                 (q.half(), None, pos, 5e6, sec, out.half(), None),
+                 (q, q, pos, 5e6, sec, out, None),
+                 (q, None, pos, 5e6, sec, q[:, :, :1].expand(2, 5, 3, 256), None),
+                 (q, None, pos, 5e6, (24, 20, 200), out, None),
+                 (q.transpose(2, 3), None, pos, 5e6, (1, 0, 0), out.transpose(2, 3), None)):
+        with pytest.raises(ig4.Ig4Error) as e:
+            ig4.ig4_mrope_rotate(*args)
+        assert e.value.status == ig4.IG4_ERR_INVALID_ARG
