@@ -2665,84 +2665,28 @@ constexpr int GRAD_SMS = 148;  // sm_100a
 
 // ---- few rows x NVFP4 weights
 
-template <int C, bool DUAL, typename OT>
-ig4_status launch_matvec_c(int M, int N, int K, const void *x, const MatvecWeights &w0,
-                           const MatvecWeights &w1, const float *bias, void *out, int cluster,
-                           int warps, cudaStream_t st) {
-  DeviceInfo *di = nullptr;
-  IG4_TRY(device_info(&di));
-  const int smem = matvec_smem(C, warps);
-  auto kern = nvfp4_matvec_kernel<C, DUAL, OT>;
-  IG4_TRY(allow_smem(kern, smem));
-  const int tiles = (N + 127) / 128 * 8;
-  cudaLaunchConfig_t lc = {};
-  lc.blockDim = dim3(32 * warps);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  lc.attrs = attr;
-  lc.numAttrs = cluster > 1 ? 2 : 1;
-  // Row tiles are dealt out in advance, so all clusters have to run at once:
-  // as many as the device holds (fewer than its SMs would suggest where a
-  // cluster does not fit the rest of a GPC), a fact of kernel and device.
-  static std::atomic<int> fit[MAX_DEVICES][4][MATVEC_MAX_WARPS + 1];
-  const int lg = cluster == 1 ? 0 : cluster == 2 ? 1 : cluster == 4 ? 2 : 3;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return IG4_ERR_CUDA;
-  std::atomic<int> &known = fit[dev][lg][warps];
-  int most = known.load(std::memory_order_relaxed);
-  if (most == 0) {
-    if (cluster == 1) {
-      int per_sm = 0;
-      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, 32 * warps, smem) !=
-          cudaSuccess)
-        return IG4_ERR_CUDA;
-      most = per_sm * di->sms;
-    } else {
-      lc.gridDim = dim3(2 * di->sms / cluster * cluster);
-      if (cudaOccupancyMaxActiveClusters(&most, kern, &lc) != cudaSuccess) return IG4_ERR_CUDA;
-    }
-    if (most < 1) return IG4_ERR_CUDA;
-    known.store(most, std::memory_order_relaxed);
-  }
-  lc.gridDim = dim3(std::min(tiles, most) * cluster);
-  if (cudaLaunchKernelEx(&lc, kern, static_cast<const __nv_bfloat16 *>(x), w0, w1, bias,
-                         static_cast<OT *>(out), M, N, K, tiles, cluster) != cudaSuccess)
-    return IG4_ERR_CUDA;
-  return last_launch_status();
-}
-
-// Warps of a CTA and CTAs of a cluster.  The clusters that run at once take the
-// row tiles in rounds, and a round lasts as long as its SM's warps need for their
-// chunks: the choice with the least rounds x chunks x warps on an SM, at least 12
-// of them counted (fewer do not hide their latency).  Full width: 12 warps and no
-// cluster for K = 4608 (4608 rows: 6.5 us, 7.7 with 8 warps in clusters of 2; the
-// gated pair 26.6 and 27.7), 16 warps in clusters of 2 for K = 12288 (13.1 us, 13.6
-// with 8 in clusters of 4, of which 71 fit and 72 would have to).
+// CTAs of a cluster (which split K), stages of the weights' ring.  The `fit`
+// clusters that run at once take the row tiles in rounds; in clocks: a round
+// streams a CTA's k-blocks (200 each) and hands its sums over (2500 between CTAs,
+// 1000 without; hidden behind the next round's streaming where that is longer);
+// in front of the first, the digits (60 per row and k-block).
 struct MatvecPlan {
-  int warps, cluster, chunks;
+  int cluster, stages;
 };
-MatvecPlan matvec_plan(int nc, long tiles) {
+MatvecPlan matvec_plan(int M, int mats, int nkb, long tiles, const int (&fit)[MATVEC_MAX_CLUSTER + 1]) {
   MatvecPlan best{};
   long best_cost = 0;
-  for (int cl = 1; cl <= MATVEC_MAX_CLUSTER; cl *= 2) {
-    for (int w = MATVEC_MIN_WARPS; w <= MATVEC_MAX_WARPS; ++w) {
-      const int chunks = (nc + cl * w - 1) / (cl * w);
-      if (chunks > MATVEC_MAX_CHUNKS) continue;
-      const int per_sm = w == MATVEC_MIN_WARPS ? 2 : 1;
-      // (clusters of 4 and 8 do not fill every GPC)
-      const long at_once = std::max(1, per_sm * (cl <= 2 ? GRAD_SMS : cl == 4 ? 142 : 128) / cl);
-      const long cost = (tiles + at_once - 1) / at_once * chunks * std::max(12, per_sm * w);
-      if (best.warps == 0 || cost < best_cost) {
-        best = {w, cl, chunks};
-        best_cost = cost;
-      }
+  for (int c = 1; c <= MATVEC_MAX_CLUSTER && c <= nkb; ++c) {
+    const int kbs = (nkb + c - 1) / c, each = (128 + c - 1) / c;
+    const int left = MATVEC_SMEM - 1024 - matvec_digit_bytes(M, kbs) - matvec_sum_bytes(M, mats, c, each);
+    const int stages = std::min(MATVEC_MAX_STAGES, left / MATVEC_STAGE_BYTES);
+    if (kbs * M > MATVEC_MAX_ITEMS * MATVEC_DIGIT_WARPS || stages < MATVEC_MIN_STAGES || fit[c] < 1) continue;
+    const long rounds = (tiles + fit[c] - 1) / fit[c];
+    const long stream = 200L * kbs * mats, sums = c > 1 ? 2500 : 1000;
+    const long cost = (rounds - 1) * std::max(stream, sums) + stream + sums + 60L * kbs * M;
+    if (best.cluster == 0 || cost < best_cost) {
+      best = {c, stages};
+      best_cost = cost;
     }
   }
   return best;
@@ -2751,13 +2695,58 @@ MatvecPlan matvec_plan(int nc, long tiles) {
 template <bool DUAL, typename OT>
 ig4_status launch_matvec(int M, int N, int K, const void *x, const MatvecWeights &w0,
                          const MatvecWeights &w1, const float *bias, void *out, cudaStream_t st) {
-  const int nc = (K + MATVEC_CHUNK - 1) / MATVEC_CHUNK;
-  const MatvecPlan p = matvec_plan(nc, (N + 127L) / 128 * 8);
-  switch (p.chunks) {
-    case 1: return launch_matvec_c<1, DUAL, OT>(M, N, K, x, w0, w1, bias, out, p.cluster, p.warps, st);
-    case 2: return launch_matvec_c<2, DUAL, OT>(M, N, K, x, w0, w1, bias, out, p.cluster, p.warps, st);
-    default: return launch_matvec_c<3, DUAL, OT>(M, N, K, x, w0, w1, bias, out, p.cluster, p.warps, st);
+  constexpr int MATS = DUAL ? 2 : 1;
+  DeviceInfo *di = nullptr;
+  IG4_TRY(device_info(&di));
+  auto kern = nvfp4_matvec_kernel<DUAL, OT>;
+  IG4_TRY(allow_smem(kern, MATVEC_SMEM));
+  cudaLaunchConfig_t lc = {};
+  lc.blockDim = dim3(MATVEC_THREADS);
+  lc.dynamicSmemBytes = MATVEC_SMEM;
+  lc.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  // Clusters of each size the device holds at once (fewer than its SMs would suggest
+  // where a cluster does not fit the rest of a GPC), a fact of kernel and device.
+  static std::atomic<int> known[MAX_DEVICES][MATVEC_MAX_CLUSTER + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= MAX_DEVICES) return IG4_ERR_CUDA;
+  int fit[MATVEC_MAX_CLUSTER + 1] = {0, di->sms};
+  for (int c = 2; c <= MATVEC_MAX_CLUSTER; ++c) {
+    fit[c] = known[dev][c].load(std::memory_order_relaxed);
+    if (fit[c] == 0) {
+      lc.gridDim = dim3(di->sms / c * c);
+      attr[1].val.clusterDim.x = c;
+      lc.numAttrs = 2;
+      if (cudaOccupancyMaxActiveClusters(&fit[c], kern, &lc) != cudaSuccess || fit[c] < 1)
+        return IG4_ERR_CUDA;
+      known[dev][c].store(fit[c], std::memory_order_relaxed);
+    }
   }
+  const int tiles = (N + 127) / 128;
+  const MatvecPlan p = matvec_plan(M, MATS, (K + 255) / 256, tiles, fit);
+  CUtensorMap t0, t1;
+  IG4_TRY(map_2d(&t0, w0.codes, 1, N, K / 2, K / 2, 128, 128));
+  if (DUAL)
+    IG4_TRY(map_2d(&t1, w1.codes, 1, N, K / 2, K / 2, 128, 128));
+  else
+    t1 = t0;
+  const int clusters = std::min(tiles, fit[p.cluster]);
+  const int each = (128 + p.cluster - 1) / p.cluster;
+  const MatvecArgs a{static_cast<const __nv_bfloat16 *>(x), {w0.sf, w1.sf}, {w0.scale, w1.scale},
+                     bias, out, M, N, K, tiles, p.cluster, clusters, p.stages,
+                     ((K + 255) / 256 + p.cluster - 1) / p.cluster, each, matvec_divider(M),
+                     matvec_divider(p.cluster), matvec_divider(each)};
+  attr[1].val.clusterDim.x = p.cluster;
+  lc.numAttrs = p.cluster > 1 ? 2 : 1;
+  lc.gridDim = dim3(clusters * p.cluster);
+  if (cudaLaunchKernelEx(&lc, kern, t0, t1, a) != cudaSuccess) return IG4_ERR_CUDA;
+  return last_launch_status();
 }
 
 bool matvec_args_ok(int M, int N, int K, const void *x, const MatvecWeights *w, int n_w,

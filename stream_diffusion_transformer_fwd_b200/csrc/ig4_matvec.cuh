@@ -3,71 +3,50 @@
 // of a feed-forward layer: u = silu(x Wg^T) * (x Wu^T).
 //
 // Each weight is used M <= 8 times, so the weight bytes (4.5 bits per weight)
-// would bound it, 41 weights a clock and SM; what does is the products' rate.
-// They run on mma.sync m16n8k16, the weights as the 16-row operand and the M
-// rows as its 8 columns: a lane's 16 loaded bytes become its own operand
-// registers, with nothing staged between decoding and product.  That instruction
-// takes 32 clocks of a quarter SM here: 32 weights a clock and SM, 21 reached
-// (16384 x 12288 weights: 35 us; 4608 x 12288: 13.1 us).  Decoding into tensor
-// memory for tcgen05.mma instead, which has no such limit, took 25 us for the
-// latter: its hand-shakes per 64 elements and a CTA's start cost more than they
-// gain at these sizes.
+// bound it, as long as nothing touches the weights one by one: decoded into
+// registers for mma.sync they came at 21 weights a clock and SM, where HBM delivers
+// 41.  So the weights stay as they are: a tile of 128 rows is the A operand of
+// block-scaled FP4 MMAs (kind::mxf4nvf4), codes by TMA, scales by bulk copy and
+// tcgen05.cp.  It is x that is brought into the form of the B operand (below).
+// Measured, mma.sync form -> this one: one row, 16384 x 12288 weights 35.5 -> 24.4 us
+// (4.7 TB/s), gated pair at 12288 x 4608 26.2 -> 16.4 us (3.9 TB/s), of 8 rows 26.5 ->
+// 20.5, one row by 4608 x 12288 13.9 -> 12.5, 8 rows 15.0 -> 15.5; a call of a few
+// hundred kilobytes 2.6 -> 4.2 us.  About 4 us of each are launch, digits, the first
+// loads' latency and the exchange of sums.
 //
-// The order of the contraction is free: lane (g, t) of a warp takes 32
-// consecutive codes of weight rows g and g + 8 (one 16-byte load each) and the
-// same 32 elements of x row g, four per MMA, paired as its codes come out.
+// A row's slice of x becomes a fixed-point number per element, v = RN(x 2^sh),
+// |v| < 2^22 for the largest, written with eight digits d_p in -4 .. 3 to the base
+// 8: v = sum_p d_p 8^p.  E2M1 holds d / 2 exactly (0, 1/2, 1, 3/2, 2), so the
+// digits of plane p are row 8 m + p of B, all its block scales 1, and
+//   sum_k x W = 2^(1 - sh) sum_p 8^p (sum_k (d_p / 2) W):
+// the tensor cores' products are exact and summed in fp32, the eight planes' sums
+// are added in fp32.  x is exact down to 2^-13 of its slice's largest element,
+// rounded at 2^-22 of it below.  The MMA's columns are free: with 8, 64 or 256 of them
+// a k-block takes the same time, that of issuing its MMAs.
 //
-// Codes become fp16 pairs two ways.  cvt.f16x2.e2m1x2 takes two codes per
-// instruction, but at 16 lanes per clock and SM: with it alone that pipe was 80%
-// busy and bounded the kernel.  Or in the integer pipe: a nibble s|ee|m moved to
-// bits 15 and 11..9 is the fp16 number +-code * 2^-14 (the exponent field ee and
-// one mantissa bit; ee = 0 is an fp16 subnormal, as it should be), two masks and
-// two shifts for a pair.  MATVEC_CVT_WORDS of a lane's four 8-code words take the
-// first way, which keeps both pipes below the weights' time.
-//
-// Exactness: code times group scale has at most 6 significant bits between
-// 2^-10 and 2688; both ways form it times 2^-9 in fp16, between 2^-19 and 5.25:
-// exact.  x (8 significant bits) is multiplied by a power of two per row and
-// warp that brings its largest element into [2^14, 2^15) before it becomes fp16:
-// exact down to 2^-28 of that element, rounded at 2^-39 of it below.  Sums are
-// fp32.
-//
-// Weights arrive by cp.async in a ring of shared-memory stages; a lane copies
-// what it will read itself, so the ring needs no barrier, and the first stages
-// are on their way before x is read.  (With one tile prefetched into registers
-// 4608 x 12288 weights took 18 us.)  A warp keeps its slice of x in registers for
-// all the weight rows it meets (read from shared memory per use, x of 8 rows made
-// the gated pair at full width take 33 us instead of 28); a CTA's 8 to 16 warps
-// split K, and for long K (or few rows) the CTAs of a cluster split it further and
-// exchange partial sums through distributed shared memory.  16-row tiles take rows
-// {4j .. 4j+3} + {0, 32, 64, 96} of a 128-row block: their 16 scale words of a
-// k-block are then 64 consecutive bytes in the packed order.
+// A cluster's CTAs split K, each keeps the digits of its slice in shared memory
+// for all row tiles it meets, and they add up their sums through distributed
+// shared memory, each CTA a share of the rows.
 #pragma once
 
-#include <cuda_fp16.h>
-
+#include "ig4_gemm.cuh"
 #include "ig4_ptx.cuh"
 
 namespace ig4 {
 
-constexpr int MATVEC_MIN_WARPS = 8;  // two CTAs of these fit an SM, one of more warps
-constexpr int MATVEC_MAX_WARPS = 16;
-constexpr int MATVEC_CHUNK = 128;    // k elements of a warp step: 4 lanes x 32
-constexpr int MATVEC_MAX_CHUNKS = 3; // per warp
+constexpr int MATVEC_THREADS = 512;  // warps 0-3 epilogue, 4 loads, 5-8 MMAs; all but 4 make digits
+constexpr int MATVEC_DIGIT_WARPS = 15;
+constexpr int MATVEC_MAX_ITEMS = 10;  // (row, 256-element k-block) pairs per warp
+constexpr int MATVEC_MAX_ISSUERS = 4;  // even: an issuer of the gated pair meets one matrix only
+constexpr int MATVEC_MIN_STAGES = MATVEC_MAX_ISSUERS;
 constexpr int MATVEC_MAX_CLUSTER = 8;
-constexpr int MATVEC_MAX_K = 24576;  // what the widest clusters of the fewest warps hold
-constexpr int MATVEC_BATCH = 4;      // row tiles per exchange between the CTAs of a cluster
-constexpr int MATVEC_CVT_WORDS = 3;  // of a lane's four code words
-constexpr int MATVEC_STAGES = 3;
-// a stage: per warp, chunk and row half 32 x 16 code bytes, then 32 x 4 scale bytes
-constexpr int MATVEC_UNIT_BYTES = 32 * 16 + 32 * 4;
-__host__ __device__ constexpr int matvec_stage_bytes(int chunks, int warps) {
-  return warps * chunks * 2 * MATVEC_UNIT_BYTES;
-}
-// the ring, then the warps' sums of two items, twice
-__host__ __device__ constexpr int matvec_smem(int chunks, int warps) {
-  return MATVEC_STAGES * matvec_stage_bytes(chunks, warps) + 2 * 2 * warps * 128 * 4;
-}
+constexpr int MATVEC_MAX_K = 24576;
+constexpr int MATVEC_STAGE_BYTES = 16384 + 2048;  // codes, scales of 128 rows x 256 elements
+constexpr int MATVEC_MAX_STAGES = 10;
+constexpr int MATVEC_SMEM = 224 << 10;  // dynamic
+// TMEM: 256 columns of accumulators, then scales
+constexpr uint32_t MATVEC_SF_COL = 256;
+constexpr uint32_t MATVEC_ONES_COL = MATVEC_SF_COL + 16 * MATVEC_MAX_STAGES;
 
 struct MatvecWeights {
   const uint8_t *codes;
@@ -75,298 +54,435 @@ struct MatvecWeights {
   const float *scale;
 };
 
-__device__ __forceinline__ void cp_async16(void *dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Two E2M1 codes (byte `i` of w, low nibble first) as an fp16 pair
-template <int i>
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t w) {
-  uint32_t r;
-  if constexpr (i == 0)
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
-  else if constexpr (i == 1)
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
-  else if constexpr (i == 2)
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, c;\n\t}" : "=r"(r) : "r"(w));
-  else
-    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, d;\n\t}" : "=r"(r) : "r"(w));
-  return r;
-}
-// Codes J and J + 4 of a word (nibble 0 lowest) times 2^-14 as an fp16 pair
-template <int J>
-__device__ __forceinline__ uint32_t e2m1_pair(uint32_t w) {
-  const uint32_t mag = J < 3 ? w << (J < 3 ? 9 - 4 * J : 0) : w >> 3;
-  const uint32_t sign = w << (12 - 4 * J);
-  return (mag & 0x0E000E00u) | (sign & 0x80008000u);
-}
-__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+struct MatvecArgs {
+  const __nv_bfloat16 *x;
+  const uint8_t *sf[2];
+  const float *scale[2];
+  const float *bias;
+  void *out;
+  int M, N, K;
+  int tiles, cluster, clusters, stages;
+  int kbs;        // k-blocks of a CTA, at most
+  int rows_each;  // of a tile's 128 rows, added up by one CTA of the cluster
+  // dividers by M, cluster and rows_each: (i * m) >> 16 (an integer division takes about
+  // 100 clocks, and there were 30 in front of the first product)
+  int div_m, div_cluster, div_rows;
+};
+constexpr int MATVEC_DIV = 65536;
+__host__ __device__ constexpr int matvec_divider(int n) { return (MATVEC_DIV + n - 1) / n; }
+__host__ __device__ constexpr int matvec_digit_bytes(int M, int kblocks) { return M * kblocks * 1024; }
+__host__ __device__ constexpr int matvec_sum_bytes(int M, int mats, int cluster, int rows_each) {
+  return cluster > 1 ? 2 * cluster * mats * M * rows_each * 4 : 0;
 }
 
-// C: 128-element chunks of K per warp.  DUAL: w[0] gate, w[1] up.
-template <int C, bool DUAL, typename OT>
-__global__ void __launch_bounds__(32 * MATVEC_MAX_WARPS, 1)
-    nvfp4_matvec_kernel(const __nv_bfloat16 *x, MatvecWeights w0, MatvecWeights w1,
-                        const float *bias, OT *out, int M, int N, int K, int n_tiles, int cluster) {
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// All threads of the cluster meet, without ordering their memory accesses (which would
+// wait for the outputs' stores)
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// Digits of u = v + 04444 4444 (octal: 4 in every digit): octal digit p of u in
+// nibble p, less 4, as an E2M1 code of half its value.  (Bits above a digit's
+// three may be set in between; the masks of the last step drop them.)
+__device__ __forceinline__ uint32_t octal_codes(uint32_t u) {
+  u = (u & 0x0000FFFFu) | ((u << 4) & 0xFFFF0000u);
+  u = (u & 0x00FF00FFu) | ((u << 2) & 0xFF00FF00u);
+  u = (u & 0x0F0F0F0Fu) | ((u << 1) & 0xF0F0F0F0u);
+  const uint32_t neg = (~u & 0x44444444u) >> 2;           // 1 in every digit below 4
+  return (((u & 0x33333333u) ^ (3 * neg)) + neg) | (neg << 3);  // 4 - d = (3 - d) + 1, sign
+}
+
+// 8 x 8 nibbles transposed: nibble i of w[p] and nibble p of w[i] change places
+__device__ __forceinline__ void transpose_nibbles(uint32_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = w[i], b = w[i + 4];
+    w[i] = __byte_perm(a, b, 0x5410);
+    w[i + 4] = __byte_perm(a, b, 0x7632);
+  }
+#pragma unroll
+  for (int h = 0; h < 8; h += 4)
+#pragma unroll
+    for (int i = h; i < h + 2; ++i) {
+      const uint32_t a = w[i], b = w[i + 2];
+      w[i] = __byte_perm(a, b, 0x6240);
+      w[i + 2] = __byte_perm(a, b, 0x7351);
+    }
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const uint32_t a = w[i], b = w[i + 1];
+    w[i] = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+    w[i + 1] = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+  }
+}
+
+// DUAL: tm0, sf[0], scale[0] gate, tm1, .. up.
+template <bool DUAL, typename OT>
+__global__ void __launch_bounds__(MATVEC_THREADS, 1)
+    nvfp4_matvec_kernel(const __grid_constant__ CUtensorMap tm0, const __grid_constant__ CUtensorMap tm1,
+                        const __grid_constant__ MatvecArgs a) {
   constexpr int MATS = DUAL ? 2 : 1;
-  constexpr int BATCH = MATVEC_BATCH / MATS;
-  extern __shared__ uint4 ring[];
-  const int warps = blockDim.x >> 5;
-  const int STAGE = matvec_stage_bytes(C, warps);
-  // [parity][item][warp][128]
-  float *red = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(ring) + MATVEC_STAGES * STAGE);
-  __shared__ float psum[2][BATCH][MATS][128];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = align1024(smem_raw);
+  __shared__ uint64_t full[MATVEC_MAX_STAGES], empty[MATVEC_MAX_STAGES], tfull[2], tempty[2];
+  __shared__ uint64_t sum_full[2], sum_empty[2], drain;
+  __shared__ uint32_t tmem_slot, amax[8];
+  __shared__ float inv[2][8];
+  __shared__ int abort_word;
+  __shared__ alignas(128) uint32_t ones[128];
+  volatile int *abort_flag = &abort_word;
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int g = lane >> 2, t = lane & 3;
+  const int cluster = a.cluster;
   const int rank = cluster > 1 ? static_cast<int>(cluster_ctarank()) : 0;
-  const int cl = blockIdx.x / cluster, n_cl = gridDim.x / cluster;
+  const int cl = (static_cast<int>(blockIdx.x) * a.div_cluster) >> 16, n_cl = a.clusters;
+  const int nkb = (a.K + 255) / 256;
+  const int kb0 = (nkb * rank * a.div_cluster) >> 16, kb1 = (nkb * (rank + 1) * a.div_cluster) >> 16;
+  const int M = a.M, N = a.N, K = a.K;
+  uint8_t *sB = smem;  // [k-block][row of x][plane][128 bytes], 128-byte swizzle
+  uint8_t *sA = sB + matvec_digit_bytes(M, a.kbs);
+  float *sums = reinterpret_cast<float *>(sA + a.stages * MATVEC_STAGE_BYTES);
+  // What streams is stages: the k-blocks of a tile, gate and up in turn for DUAL.  A
+  // thread takes 930 clocks to issue a stage's four copies and four MMAs, more than
+  // HBM needs to bring it (800), so `issuers` warps take the stages in turn, each with
+  // an accumulator of its own, and that twice, so that a tile's sums are read while the
+  // next tile's grow.  (One accumulator for each of four issuers at M > 4: 16384 x 12288
+  // weights 35 us instead of 32.)
+  const int per_tile = (kb1 - kb0) * MATS;
+  const int width = M > 4 ? 64 : 32, slots = M > 4 ? 2 : MATVEC_MAX_ISSUERS;
+  const int issuers = min(slots, per_tile);
+  // A stage always has the same issuer: loads may land out of order, and a parity wait
+  // cannot tell a stage's use from the one two before, so who waits for a use must
+  // have seen the one before it.
+  const int stages = issuers == 3 ? a.stages / 3 * 3 : a.stages & -issuers;
+  // 64-element steps of a k-block (the last may be short)
+  auto steps = [&](int kb) { return min(4, K / 64 - 4 * kb); };
+
+  // The thread that loads prepares the barriers itself, so that weights and x are on
+  // their way while the CTA (and its peers) set up the rest.
+  if (warp == 4 && lane == 0) {
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], issuers);
+      mbar_init(&tempty[b], 128);
+      mbar_init(&sum_full[b], 4 * cluster);
+      mbar_init(&sum_empty[b], 4 * cluster);
+    }
+    mbar_init(&drain, issuers);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm0);
+    if constexpr (DUAL) tma_prefetch_desc(&tm1);
+  }
+  if (threadIdx.x < 128) ones[threadIdx.x] = 0x38383838u;  // E4M3 1
+  if (threadIdx.x < 8) amax[threadIdx.x] = 0;
   pdl_wait();
   pdl_trigger();
 
-  // this warp's run of chunks
-  const int nc = (K + MATVEC_CHUNK - 1) / MATVEC_CHUNK;
-  const int slots = cluster * warps, slot = rank * warps + warp;
-  const int c0 = nc * slot / slots, c1 = nc * (slot + 1) / slots;  // at most C chunks
-
-  const int nch = c1 - c0;
-
-  // items of this cluster: its row tiles, gate then up for DUAL
-  const int local_tiles = (n_tiles - cl + n_cl - 1) / n_cl;
-  const int items = local_tiles * MATS;
-  // A lane's unit of stage s, chunk c, row half h (weight rows g and g + 8 of the
-  // tile, two 32-row quarters apart).  Rows past N read row N - 1 and are not
-  // stored; the lanes whose half of the last chunk is past K read the other half
-  // and have zero x.
-  uint8_t *wring = reinterpret_cast<uint8_t *>(ring) + warp * (C * 2 * MATVEC_UNIT_BYTES);
-  const int past = K % MATVEC_CHUNK != 0 && c1 == nc && t >= 2 ? 64 : 0;  // of chunk nch - 1
-  auto fetch = [&](int it) {
-    if (it < items) {
-      const MatvecWeights &w = (DUAL && (it & 1)) ? w1 : w0;
-      const int tile = cl + (it / MATS) * n_cl;
-      const int j4 = 4 * (tile & 7) + (g & 3);
-      uint8_t *st = wring + (it % MATVEC_STAGES) * STAGE;
-      const uint8_t *sp = w.sf + 512 * (static_cast<long>(tile >> 3) * (K / 64) + 2 * c0 + (t >> 1)) +
-                          16 * j4 + 4 * (g >> 2);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = min((tile >> 3) * 128 + 32 * (g >> 2) + 64 * h + j4, N - 1);
-        const uint8_t *cp = w.codes + static_cast<long>(row) * (K / 2) + c0 * 64 + 16 * t;
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-          if (c >= nch) break;
-          uint8_t *u = st + (c * 2 + h) * MATVEC_UNIT_BYTES;
-          const int back = c == nch - 1 ? past : 0;
-          cp_async16(u + 16 * lane, cp + c * 64 - back / 2);
-          cp_async4(u + 512 + 4 * lane, sp + c * 1024 + 8 * h - back * 8);
-        }
-      }
+  // ---------------- loads, in the order of the MMAs: tiles, k-blocks, matrices.
+  // One thread's instructions are the limit here and at the MMAs (about 5 clocks
+  // each): addresses advance by additions.
+  int ld_row = cl * 128, ld_c0 = kb0 * 128, ld_s = 0, ld_mat = 0;
+  uint32_t ld_ph = 0, ld_sf_bytes = steps(kb0) * 512;
+  const long sf_first = (static_cast<long>(cl) * (K / 64) + 4 * kb0) * 512;
+  const long sf_tile = static_cast<long>(n_cl) * (K / 64) * 512;
+  const uint8_t *sf0 = a.sf[0] + sf_first, *sf1 = a.sf[1] + sf_first;  // of this tile
+  const int ld_rows = a.tiles * 128, c0_end = kb1 * 128;
+  long ld_off = 0;  // of this k-block in the tile's scales
+  uint8_t *ld_st = sA;
+  auto issue = [&]() {
+    uint64_t *bar = &full[ld_s];
+    mbar_arrive_expect_tx(bar, 16384 + ld_sf_bytes);
+    if (DUAL && ld_mat) {
+      tma_load_2d(ld_st, &tm1, bar, ld_c0, ld_row);
+      bulk_load(ld_st + 16384, sf1 + ld_off, ld_sf_bytes, bar);
+    } else {
+      tma_load_2d(ld_st, &tm0, bar, ld_c0, ld_row);
+      bulk_load(ld_st + 16384, sf0 + ld_off, ld_sf_bytes, bar);
     }
-    cp_async_commit();
+    ld_st += MATVEC_STAGE_BYTES;
+    if (++ld_s == stages) {
+      ld_s = 0;
+      ld_st = sA;
+      ld_ph ^= 1;
+    }
+    if (DUAL && (ld_mat ^= 1)) return;
+    ld_c0 += 128;
+    ld_off += 2048;
+    if (ld_c0 == c0_end) {
+      ld_c0 = kb0 * 128;
+      ld_off = 0;
+      ld_row += n_cl * 128;
+      sf0 += sf_tile;
+      sf1 += sf_tile;
+    }
+    ld_sf_bytes = min(2048, 8 * K - 16 * ld_c0);  // 8 bytes per element of K
   };
+  if (warp == 4 && lane == 0)
+    for (int i = 0; i < stages && ld_row < ld_rows; ++i) issue();
+  // x: an item (k-block, row) per warp and step
+  const int items = (kb1 - kb0) * M, w0 = warp - (warp > 4);
+  uint4 v[MATVEC_MAX_ITEMS];
 #pragma unroll
-  for (int i = 0; i < MATVEC_STAGES - 1; ++i) fetch(i);
-
-  // x slice: 16 fp16 pairs per chunk, scaled by 2^sh; inv0, inv1 undo it for
-  // the accumulator's columns (tokens 2t, 2t + 1)
-  uint32_t xb[C][16];
-  float inv0, inv1;
-  {
-    float amax = 0.0f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int k = (c0 + c) * MATVEC_CHUNK + 32 * t;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (c0 + c < c1 && k < K && g < M)
-          v = __ldg(reinterpret_cast<const uint4 *>(x + static_cast<long>(g) * K + k) + i);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          xb[c][4 * i + e] = u[e];
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(u[e] << 16)),
-                                   fabsf(__uint_as_float(u[e] & 0xFFFF0000u))));
-        }
-      }
+  for (int t = 0; t < MATVEC_MAX_ITEMS; ++t) {
+    const int i = w0 + MATVEC_DIGIT_WARPS * t;
+    v[t] = make_uint4(0, 0, 0, 0);
+    if (warp != 4 && i < items) {
+      const int b = (i * a.div_m) >> 16, m = i - b * M;
+      const int k = (kb0 + b) * 256 + 8 * lane;
+      if (k < K) v[t] = __ldg(reinterpret_cast<const uint4 *>(a.x + m * K + k));
     }
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;  // -127 for zero
-    const int sh = min(14 - ex, 126);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-    const float inv = __uint_as_float(static_cast<uint32_t>(127 + 9 - sh) << 23);
-    inv0 = __shfl_sync(0xffffffffu, inv, 8 * t);
-    inv1 = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const __half2 h = __floats2half2_rn(__uint_as_float(xb[c][i] << 16) * up,
-                                            __uint_as_float(xb[c][i] & 0xFFFF0000u) * up);
-        xb[c][i] = *reinterpret_cast<const uint32_t *>(&h);
-      }
-    // the integer way yields codes (0, 4), (1, 5), (2, 6), (3, 7) of a word
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int i = 4 * MATVEC_CVT_WORDS; i < 16; i += 4) {
-        const uint32_t p0 = xb[c][i], p1 = xb[c][i + 1], p2 = xb[c][i + 2], p3 = xb[c][i + 3];
-        xb[c][i] = __byte_perm(p0, p2, 0x5410);
-        xb[c][i + 1] = __byte_perm(p0, p2, 0x7632);
-        xb[c][i + 2] = __byte_perm(p1, p3, 0x5410);
-        xb[c][i + 3] = __byte_perm(p1, p3, 0x7632);
-      }
   }
-
-  const int o = threadIdx.x & 127;  // output of a tile: row o / 8, token o % 8
-  auto finish = [&](int tl, float v0, float v1) {
-    const int tile = cl + tl * n_cl, rho = o >> 3, m = o & 7;
-    const int row = (tile >> 3) * 128 + 32 * (rho >> 2) + 4 * (tile & 7) + (rho & 3);
-    if (row >= N || m >= M) return;
-    float v;
-    if constexpr (DUAL)
-      v = silu_f(v0 * __ldg(w0.scale + row)) * (v1 * __ldg(w1.scale + row));
-    else
-      v = fmaf(v0, __ldg(w0.scale + row), bias != nullptr ? __ldg(bias + row) : 0.0f);
-    OT *op = out + static_cast<long>(m) * N + row;
-    if constexpr (sizeof(OT) == 4)
-      *op = v;
-    else
-      *op = __float2bfloat16_rn(v);
-  };
-  // two items per step: gate and up of a tile, or two tiles
-  for (int i0 = 0; i0 < items; i0 += 2) {
-    const int par = (i0 >> 1) & 1;
-#pragma unroll 1
-    for (int it = i0; it < i0 + 2 && it < items; ++it) {
-      cp_async_wait<MATVEC_STAGES - 2>();
-      fetch(it + MATVEC_STAGES - 1);
-      const uint8_t *st = wring + (it % MATVEC_STAGES) * STAGE;
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < C; ++c) {
-        if (c >= nch) break;
-        uint32_t s[2][2];  // row half, group
-        uint4 q[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint8_t *u = st + (c * 2 + h) * MATVEC_UNIT_BYTES;
-          q[h] = *reinterpret_cast<const uint4 *>(u + 16 * lane);
-          const uint16_t two = *reinterpret_cast<const uint16_t *>(u + 512 + 4 * lane + 2 * (t & 1));
-          uint32_t f;
-          asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(two));
-          s[h][0] = __byte_perm(f, 0, 0x1010);
-          s[h][1] = __byte_perm(f, 0, 0x3232);
-        }
-        const uint32_t qa[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
-        const uint32_t qb[4] = {q[1].x, q[1].y, q[1].z, q[1].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // words 0, 1 are group 0, words 2, 3 group 1
-          const bool cvt = i < MATVEC_CVT_WORDS;
-          const uint32_t f = cvt ? 0x18001800u : 0x50005000u;  // 2^-9 or 2^5
-          const uint32_t sa = hmul2_u(s[0][i >> 1], f), sb = hmul2_u(s[1][i >> 1], f);
-          uint32_t a[4], b[4];
-          if (cvt) {
-            a[0] = e2m1x2_to_f16x2<0>(qa[i]);
-            a[1] = e2m1x2_to_f16x2<1>(qa[i]);
-            a[2] = e2m1x2_to_f16x2<2>(qa[i]);
-            a[3] = e2m1x2_to_f16x2<3>(qa[i]);
-            b[0] = e2m1x2_to_f16x2<0>(qb[i]);
-            b[1] = e2m1x2_to_f16x2<1>(qb[i]);
-            b[2] = e2m1x2_to_f16x2<2>(qb[i]);
-            b[3] = e2m1x2_to_f16x2<3>(qb[i]);
-          } else {
-            a[0] = e2m1_pair<0>(qa[i]);
-            a[1] = e2m1_pair<1>(qa[i]);
-            a[2] = e2m1_pair<2>(qa[i]);
-            a[3] = e2m1_pair<3>(qa[i]);
-            b[0] = e2m1_pair<0>(qb[i]);
-            b[1] = e2m1_pair<1>(qb[i]);
-            b[2] = e2m1_pair<2>(qb[i]);
-            b[3] = e2m1_pair<3>(qb[i]);
-          }
-          mma_f16(acc, hmul2_u(a[0], sa), hmul2_u(b[0], sb), hmul2_u(a[1], sa), hmul2_u(b[1], sb),
-                  xb[c][4 * i], xb[c][4 * i + 1]);
-          mma_f16(acc, hmul2_u(a[2], sa), hmul2_u(b[2], sb), hmul2_u(a[3], sa), hmul2_u(b[3], sb),
-                  xb[c][4 * i + 2], xb[c][4 * i + 3]);
-        }
-      }
-      float *rw = red + ((2 * par + (it & 1)) * warps + warp) * 128;
-      *reinterpret_cast<float2 *>(rw + 8 * g + 2 * t) = make_float2(acc[0] * inv0, acc[1] * inv1);
-      *reinterpret_cast<float2 *>(rw + 8 * (g + 8) + 2 * t) =
-          make_float2(acc[2] * inv0, acc[3] * inv1);
-    }
+  if (warp == 5) {
+    tmem_alloc(&tmem_slot, 512);
+    tmem_relinquish();
+  }
+  __syncwarp();
+  tc_fence_before();
+  if (cluster > 1)
+    cluster_sync_all();  // peers' barriers are set up
+  else
     __syncthreads();
-    // thread (half, o) sums output o of item i0 + half over the warps; for DUAL
-    // the first half takes both
-    const int half = threadIdx.x >> 7;  // (threads from 256 on have none)
-    float v[MATS];
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 4) {
+    __syncthreads();
+  } else {
+    // ---------------- digits of x
 #pragma unroll
-    for (int m = 0; m < MATS; ++m) {
-      v[m] = 0.0f;
-      const float *rs = red + (2 * par + (DUAL ? m : half & 1)) * warps * 128 + o;
-#pragma unroll 8
-      for (int w = 0; w < warps; ++w) v[m] += rs[w * 128];
+    for (int t = 0; t < MATVEC_MAX_ITEMS; ++t) {
+      const int i = w0 + MATVEC_DIGIT_WARPS * t;
+      if (i >= items) break;
+      const uint32_t q[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
+      uint32_t m = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m = max(m, max(q[e] & 0x7FFF0000u, (q[e] << 16) & 0x7FFF0000u));
+      m = __reduce_max_sync(0xffffffffu, m);
+      if (lane == 0) atomicMax(&amax[i - ((i * a.div_m) >> 16) * M], m);
     }
-    const int lt = DUAL ? i0 >> 1 : i0 + half;  // local tile
-    if (lt < local_tiles && half < (DUAL ? 1 : 2)) {
+    asm volatile("bar.sync 1, 480;" ::: "memory");
+    if (threadIdx.x < 8) {
+      // an infinity or a NaN in the slice: NaN; otherwise 2^(1 - sh) in two factors
+      const int ex = static_cast<int>(amax[threadIdx.x] >> 23) - 127;
+      const int sh = 21 - max(ex, -127), h = sh / 2;
+      inv[0][threadIdx.x] = ex == 128 ? __uint_as_float(0x7FC00000u)
+                                      : __uint_as_float(static_cast<uint32_t>(127 - h) << 23);
+      inv[1][threadIdx.x] = __uint_as_float(static_cast<uint32_t>(127 + 1 - (sh - h)) << 23);
+    }
+#pragma unroll
+    for (int t = 0; t < MATVEC_MAX_ITEMS; ++t) {
+      const int i = w0 + MATVEC_DIGIT_WARPS * t;
+      if (i >= items) break;
+      const int m = i - ((i * a.div_m) >> 16) * M;
+      const int ex = static_cast<int>(amax[m] >> 23) - 127;
+      const int sh = 21 - max(ex, -127), h = sh / 2;
+      const float s0 = __uint_as_float(static_cast<uint32_t>(127 + h) << 23);
+      const float s1 = __uint_as_float(static_cast<uint32_t>(127 + sh - h) << 23);
+      const uint32_t q[4] = {v[t].x, v[t].y, v[t].z, v[t].w};
+      uint32_t w[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = __uint_as_float(e & 1 ? q[e / 2] & 0xFFFF0000u : q[e / 2] << 16);
+        // 1.5 * 2^23 + v: v in the low bits of the float
+        const uint32_t f = __float_as_uint(fmaf(x * s0, s1, 12582912.0f));
+        w[e] = octal_codes(f - 0x4B400000u + 044444444u);
+      }
+      transpose_nibbles(w);
+      uint8_t *atom = sB + i * 1024 + 4 * (lane & 3);
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        *reinterpret_cast<uint32_t *>(atom + 128 * p + 16 * ((lane >> 2) ^ p)) = w[p];
+    }
+    fence_proxy_async_smem();
+    __syncthreads();
+  }
+
+  if (warp == 4) {
+    if (lane == 0) {
+      bool ok = true;
+      while (ld_row < ld_rows) {
+        // (the first `stages` loads are past; the wait is for the stage's last use)
+        if (!mbar_wait(&empty[ld_s], ld_ph ^ 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        issue();
+      }
+      if (!ok) sleep_ns(50000);  // let the loads already issued land
+    }
+  } else if (warp >= 5 && warp < 5 + issuers) {
+    if (lane == 0) {
+      const int me = warp - 5;
+      const uint32_t idesc = idesc_nvf4(128, 8 * M);
+      const uint32_t sfb = tmem + MATVEC_ONES_COL + 4 * me;
+      tmem_cp_sf(sfb, sdesc_kmajor_none(smem_u32(ones), 128));
+      // descriptors: address / 16 in the low bits
+      const uint64_t ad0 = sdesc_kmajor_sw128(smem_u32(sA)), bd0 = sdesc_kmajor_sw128(smem_u32(sB));
+      const uint64_t sd0 = sdesc_kmajor_none(smem_u32(sA) + 16384, 128);
+      int local = 0;
+      bool ok = true;
+      for (int tile = cl; tile < a.tiles && ok; tile += n_cl, ++local) {
+        const int buf = local & 1;
+        if (!mbar_wait(&tempty[buf], ((local >> 1) & 1) ^ 1, abort_flag)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (buf * slots + me) * width;
+        // of the CTA's stages this tile's are g0 .. g0 + per_tile - 1, mine the ones that
+        // are `me` modulo `issuers`
+        int first = me, s = me;
+        uint32_t ph = 0;
+        if (local > 0) {
+          const uint32_t g0 = static_cast<uint32_t>(local) * per_tile;
+          first = (me + issuers - static_cast<int>(g0 % issuers)) % issuers;
+          s = static_cast<int>((g0 + first) % stages);
+          ph = ((g0 + first) / stages) & 1;
+        }
+        for (int i = first; i < per_tile; i += issuers) {
+          if (!mbar_wait(&full[s], ph, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const int kb = static_cast<unsigned>(i) / MATS, n = steps(kb0 + kb);
+          const uint64_t ad = ad0 + s * (MATVEC_STAGE_BYTES / 16), sd = sd0 + s * (MATVEC_STAGE_BYTES / 16);
+          const uint64_t bd = bd0 + kb * (64 * M);
+          const uint32_t sfa = tmem + MATVEC_SF_COL + 16 * s;
+          if (n == 4) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tmem_cp_sf(sfa + 4 * j, sd + 32 * j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              umma_nvf4(d, ad + 2 * j, bd + 2 * j, idesc, sfa + 4 * j, sfb, i != first || j != 0);
+          } else {
+            for (int j = 0; j < n; ++j) {
+              tmem_cp_sf(sfa + 4 * j, sd + 32 * j);
+              umma_nvf4(d, ad + 2 * j, bd + 2 * j, idesc, sfa + 4 * j, sfb, i != first || j != 0);
+            }
+          }
+          umma_commit(&empty[s]);
+          s += issuers;
+          if (s >= stages) {
+            s -= stages;
+            ph ^= 1;
+          }
+        }
+        if (ok) umma_commit(&tfull[buf]);
+      }
+      umma_commit(&drain);
+      mbar_wait(&drain, 0, nullptr, WAIT_LIMIT_NS / 4);
+    }
+  } else if (warp < 4) {
+    const int r = threadIdx.x;  // row of the tile
+    const int re = a.rows_each;
+    OT *out = static_cast<OT *>(a.out);
+    // the row of a tile whose outputs this thread writes, for all rows of x or every
+    // `groups`th: its own without a cluster, else one of the CTA's share
+    const int groups = (128 * a.div_rows) >> 16;  // 1 without a cluster
+    const int group = (r * a.div_rows) >> 16, rl = r - group * re;
+    const int my_row = cluster > 1 ? rank * re + rl : r;
+    float sc0 = 0.0f, sc1 = 0.0f, bias = 0.0f;
+    auto finish = [&](int m, int row, float v0, float v1) {
+      float v;
+      if constexpr (DUAL)
+        v = silu_f(v0 * sc0) * (v1 * sc1);
+      else
+        v = fmaf(v0, sc0, bias);
+      OT *op = out + static_cast<long>(m) * N + row;
+      if constexpr (sizeof(OT) == 4)
+        *op = v;
+      else
+        *op = __float2bfloat16_rn(v);
+    };
+    int local = 0;
+    for (int tile = cl; tile < a.tiles; tile += n_cl, ++local) {
+      const int buf = local & 1;
+      const uint32_t use = static_cast<uint32_t>(local >> 1) & 1;
+      const int row = tile * 128 + my_row;
+      const bool mine = row < N && my_row < 128 && group < groups;
+      if (mine) {  // on their way while the sums grow
+        sc0 = __ldg(a.scale[0] + row);
+        if constexpr (DUAL) sc1 = __ldg(a.scale[1] + row);
+        if (!DUAL && a.bias != nullptr) bias = __ldg(a.bias + row);
+      }
+      if (!mbar_wait_warp(&tfull[buf], use, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * slots * width;
+      float y[MATS][8];
+#pragma unroll
+      for (int mat = 0; mat < MATS; ++mat)
+#pragma unroll
+        for (int c = 0; c < 8; c += 4) {
+          if (c >= M) continue;
+          float d[32];  // columns past 8 M are not used
+          tmem_ld32(acc + mat * width + 8 * c, d);
+          tmem_ld_wait();
+          for (int h = mat + MATS; h < issuers; h += MATS) {
+            float e[32];
+            tmem_ld32(acc + h * width + 8 * c, e);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) d[i] += e[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float h = d[8 * i + 7];
+#pragma unroll
+            for (int p = 6; p >= 0; --p) h = fmaf(h, 8.0f, d[8 * i + p]);
+            y[mat][c + i] = h * inv[0][c + i] * inv[1][c + i];
+          }
+        }
+      tc_fence_before();
+      mbar_arrive(&tempty[buf]);
       if (cluster == 1) {
-        finish(lt, v[0], v[MATS - 1]);
-      } else {
 #pragma unroll
-        for (int m = 0; m < MATS; ++m) psum[(lt / BATCH) & 1][lt % BATCH][m][o] = v[m];
+        for (int m = 0; m < 8; ++m)
+          if (m < M && mine) finish(m, row, y[0][m], y[MATS - 1][m]);
+        continue;
       }
-    }
-    // the cluster's CTAs add up a batch of tiles, each every `cluster`th one; a
-    // buffer is written again two batches later, after the next batch's barrier
-    const int done = DUAL ? (i0 >> 1) + 1 : min(i0 + 2, local_tiles);
-    if (cluster > 1 && (done % BATCH == 0 || done == local_tiles)) {
-      cluster_sync_all();
-      const int b = (done - 1) / BATCH;
-      for (int i = 2 * rank + half; half < 2 && i <= (done - 1) % BATCH; i += 2 * cluster) {
-        float z[2] = {0.0f, 0.0f};
-        for (int q = 0; q < cluster; ++q)
+      // every CTA's sums of rows q * rows_each + .. to CTA q:
+      // sums [buffer][from][matrix][row of x][row]
+      if (!mbar_wait_cluster_warp(&sum_empty[buf], use ^ 1, abort_flag)) break;
+      const int base = (buf * cluster + rank) * MATS * M * re + rl;
+      const uint32_t dst = map_shared_to_rank(sums + base, group);
 #pragma unroll
-          for (int m = 0; m < MATS; ++m)
-            z[m] += ld_cluster_f32(map_shared_to_rank(&psum[b & 1][i][m][o], q));
-        finish(b * BATCH + i, z[0], z[MATS - 1]);
-      }
+      for (int mat = 0; mat < MATS; ++mat)
+#pragma unroll
+        for (int m = 0; m < 8; ++m)
+          if (m < M) st_cluster_f32(dst + 4 * (mat * M + m) * re, y[mat][m]);
       __syncwarp();
+      if (lane < cluster) mbar_arrive_cluster(map_shared_to_rank(&sum_full[buf], lane));
+      if (!mbar_wait_cluster_warp(&sum_full[buf], use, abort_flag)) break;
+      if (mine) {
+        for (int m = group; m < M; m += groups) {
+          float z[2] = {0.0f, 0.0f};
+          const float *p = sums + buf * cluster * MATS * M * re + m * re + rl;
+          for (int f = 0; f < cluster; ++f)
+#pragma unroll
+            for (int mat = 0; mat < MATS; ++mat) z[mat] += p[(f * MATS + mat) * M * re];
+          finish(m, row, z[0], z[MATS - 1]);
+        }
+      }
+      if (tile + 2 * n_cl >= a.tiles) continue;  // (nobody writes this buffer again)
+      __syncwarp();
+      if (lane < cluster) mbar_arrive_cluster(map_shared_to_rank(&sum_empty[buf], lane));
     }
   }
-  if (cluster > 1) cluster_sync_all();  // shared memory stays until the last remote read
+
+  __syncwarp();
+  tc_fence_before();
+  if (cluster > 1)
+    cluster_meet();  // shared memory stays until the last remote store
+  else
+    __syncthreads();
+  tc_fence_after();
+  if (warp == 5) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace ig4

@@ -1,9 +1,11 @@
 """Few bf16 rows times NVFP4 weights against the decoded weights in 64 bits.
 
-The products are exact, so what is left is the fp32 sum: a tensor-core step of
-16 products may drop bits below 2^-23 of its largest term, 24 steps a warp, then
-at most 8 + 8 additions: under 64 * 2^-23 of the sum of the terms' absolute
-values; then eps / 2 of the stored type.
+The products are exact.  x is rounded at 2^-22 of its slice's largest element, which
+for normal numbers is under 6 of the mean magnitude: 12 * 2^-23 of the terms'
+absolute values.  In the fp32 sum a tensor-core step of 64 products may drop bits
+below 2^-23 of its largest term, at most 36 steps an accumulator at these sizes, then
+at most 3 + 7 + 8 additions: under 64 * 2^-23 of the terms' absolute values in all;
+then eps / 2 of the stored type.
 """
 
 import pytest
@@ -160,3 +162,32 @@ def test_binding_refuses(ig4):
         with pytest.raises(ig4.Ig4Error) as e:
             ig4.ig4_nvfp4_matvec(*bad)
         assert e.value.status == ig4.IG4_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 16384, 12288), (8, 16384, 12288), (3, 9216, 24576),
+                                   (5, 40000, 2048)])
+def test_more_row_tiles_than_the_device_takes_at_once(ig4, M, N, K):
+    """Several rounds of row tiles: every buffer used again and again, in step over a cluster.
+    Up to 48 steps an accumulator: 12 + 48 + 9 = 69, under 80 * 2^-23."""
+    g = gen(M + N + K)
+    codes = torch.randint(0, 256, (N, K // 2), device="cuda", generator=g, dtype=torch.uint8)
+    sf = torch.randint(0, 127, (N, K // 16), device="cuda", generator=g, dtype=torch.uint8)
+    scale = torch.rand(N, device="cuda", generator=g) + 0.5
+    packed = torch.empty(ig4.ig4_nvfp4_scale_bytes(N, K), dtype=torch.uint8, device="cuda")
+    ig4.ig4_nvfp4_pack_scales(sf, packed)
+    x = torch.randn(M, K, device="cuda", generator=g).to(torch.bfloat16)
+    out, again = (torch.full((M, N), float("nan"), device="cuda") for _ in range(2))
+    ig4.ig4_nvfp4_matvec(x, codes, packed, scale, None, out)
+    for _ in range(20):
+        ig4.ig4_nvfp4_matvec(x, codes, packed, scale, None, again)
+    done(ig4)
+    assert torch.equal(out, again)
+    value = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6],
+                         dtype=torch.float64, device="cuda")
+    for rows in torch.arange(N, device="cuda").split(2048):
+        c = codes[rows].long()
+        w = torch.stack([value[c & 15], value[c >> 4]], -1).reshape(len(rows), K)
+        w *= sf[rows].view(torch.float8_e4m3fn).double().repeat_interleave(16, 1)
+        w *= scale[rows, None].double()
+        want, size = x.double() @ w.T, x.double().abs() @ w.abs().T
+        assert torch.all((out[:, rows].double() - want).abs() <= 2.0 ** -24 * want.abs() + 80 * 2.0 ** -23 * size)
