@@ -543,11 +543,18 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
     const uint32_t tacc = tmem_base + (static_cast<uint32_t>(warp * 32) << 16);
     uint32_t local = 0;
     for (int t = blockIdx.x; t < p.items; t += gridDim.x, ++local) {
-      if (!mbar_wait_warp(&tfull, local & 1, abort_flag)) break;
-      tc_fence_after();
       const int tile = t / p.shares, z = t % p.shares;
       const int n = tile * p.R + r;  // weight row (DH: column) of this lane
       const bool valid = r < p.R && n < (DH ? p.K : p.I);
+      __nv_bfloat16 d[32];
+      auto load_du = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (valid && c + i < p.M) d[i] = du[static_cast<long>(c + i) * p.I + n];
+      };
+      if constexpr (!DH) load_du(0);  // on its way while the sums grow
+      if (!mbar_wait_warp(&tfull, local & 1, abort_flag)) break;
+      tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < p.nt; c += 32) {  // tokens c .. c + 31
         float g[32];
@@ -568,10 +575,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           tmem_ld32(tacc + 128 + c, up);
           tmem_ld_wait();
           if (!valid) continue;
-          __nv_bfloat16 d[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (c + i < p.M) d[i] = du[static_cast<long>(c + i) * p.I + n];
+          if (c > 0) load_du(c);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             if (c + i >= p.M) break;
