@@ -74,16 +74,18 @@ struct EpiSwiGLUGrad {
       tmem_ld32(tacc + c, g);
       tmem_ld32(tacc + 128 + c, up);
       tmem_ld_wait();
-      if (!valid) continue;
-      float d[32];
-      load32_bf16(du + static_cast<long>(row) * I + n + c, d);
+      if (valid) {
+        float d[32];
+        load32_bf16(du + static_cast<long>(row) * I + n + c, d);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        swiglu_grad(g[i], up[i], d[i], &g[i], &up[i]);
+        for (int i = 0; i < 32; ++i) {
+          swiglu_grad(g[i], up[i], d[i], &g[i], &up[i]);
+        }
+        __nv_bfloat16 *dst = p + static_cast<long>(row) * 2 * I + n + c;
+        store32_bf16(dst, g);
+        store32_bf16(dst + I, up);
       }
-      __nv_bfloat16 *dst = p + static_cast<long>(row) * 2 * I + n + c;
-      store32_bf16(dst, g);
-      store32_bf16(dst + I, up);
+      __syncwarp();  // tmem_ld32 takes the whole warp: rows past M wait here
     }
   }
 };
@@ -314,6 +316,7 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
           tmem_ld32(tacc + c, v);
           tmem_ld_wait();
           if (row0 + lane < p.rows && n0 + c < p.N) store32_f32(dst + c, v);
+          __syncwarp();  // tmem_ld32 takes the whole warp
         }
       } else {
 #pragma unroll 1
@@ -569,36 +572,40 @@ __global__ void __launch_bounds__(GEMM_THREADS, 1)
         tmem_ld32(tacc + c, g);
         if constexpr (DH) {
           tmem_ld_wait();
-          if (!valid) continue;
+          if (valid) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (c + i >= p.M) break;
-            if (p.shares > 1)
-              part[(static_cast<long>(z) * p.M + c + i) * p.K + n] = g[i];
-            else
-              out[static_cast<long>(c + i) * p.K + n] = __float2bfloat16_rn(g[i]);
+            for (int i = 0; i < 32; ++i) {
+              if (c + i >= p.M) break;
+              if (p.shares > 1)
+                part[(static_cast<long>(z) * p.M + c + i) * p.K + n] = g[i];
+              else
+                out[static_cast<long>(c + i) * p.K + n] = __float2bfloat16_rn(g[i]);
+            }
           }
         } else {
           float up[32];
           tmem_ld32(tacc + 128 + c, up);
           tmem_ld_wait();
-          if (!valid) continue;
-          if (c > 0) load_du(c);
+          if (valid) {
+            if (c > 0) load_du(c);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (c + i >= p.M) break;
-            float dg, dup;
-            swiglu_grad(g[i], up[i], __bfloat162float(d[i]), &dg, &dup);
-            __nv_bfloat16 *dst = out + static_cast<long>(c + i) * 2 * p.I + n;
-            dst[0] = __float2bfloat16_rn(dg);
-            dst[p.I] = __float2bfloat16_rn(dup);
+            for (int i = 0; i < 32; ++i) {
+              if (c + i >= p.M) break;
+              float dg, dup;
+              swiglu_grad(g[i], up[i], __bfloat162float(d[i]), &dg, &dup);
+              __nv_bfloat16 *dst = out + static_cast<long>(c + i) * 2 * p.I + n;
+              dst[0] = __float2bfloat16_rn(dg);
+              dst[p.I] = __float2bfloat16_rn(dup);
+            }
           }
         }
+        __syncwarp();  // tmem_ld32 takes the whole warp: lanes past the tile's rows wait here
       }
       tc_fence_before();
       mbar_arrive(&tempty);
     }
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
