@@ -140,6 +140,14 @@ EncodeTiledFn encode_fn() {
         q == cudaDriverEntryPointSuccess)
       fn = reinterpret_cast<EncodeTiledFn>(p);
   });
+  // The driver's call wants a current context, which a thread has only after a runtime
+  // call that makes one: a fresh thread's first call would fail without this.
+  thread_local bool bound = false;
+  if (!bound) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return nullptr;
+    bound = true;
+  }
   return fn;
 }
 
