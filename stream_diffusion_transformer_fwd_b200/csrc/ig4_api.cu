@@ -113,7 +113,9 @@ ig4_status device_info(DeviceInfo **out) {
 
 constexpr size_t DEFAULT_SMEM = 48 << 10;  // dynamic shared memory any kernel may use
 
-// Raise a kernel's dynamic shared-memory limit (idempotent, cheap).
+// Raise a kernel's dynamic shared-memory limit (idempotent, cheap).  `bytes` is one
+// number for all launches of a kernel: with another number for another size, a thread
+// could lower the limit between this call and the launch of a second one.
 template <typename K>
 ig4_status allow_smem(K kernel, int bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
@@ -2462,7 +2464,7 @@ struct AddNormPlan {
   int threads, grid, slots;
   size_t smem;
 };
-constexpr size_t ADDNORM_SM_SMEM = 220 << 10;
+constexpr int ADDNORM_SM_SMEM = 220 << 10;
 AddNormPlan addnorm_plan(int M, int D, size_t slot_bytes, int sms, int threads_per_sm) {
   AddNormPlan p{};
   p.warp = D <= ADDNORM_WARP_D;
@@ -2505,7 +2507,7 @@ ig4_status launch_add_norm_t(int M, int D, const void *x, const void *r, const f
                    g, eps, sp, y, scale, sfp, M, D);
   } else {
     if (p.smem > DEFAULT_SMEM)
-      IG4_TRY(allow_smem(add_rms_norm_kernel<XT, OUT>, static_cast<int>(p.smem)));
+      IG4_TRY(allow_smem(add_rms_norm_kernel<XT, OUT>, ADDNORM_SM_SMEM));
     e = launch_pdl(add_rms_norm_kernel<XT, OUT>, dim3(p.grid), dim3(p.threads), p.smem, st, xp, rp,
                    g, eps, sp, y, scale, sfp, M, D, p.slots);
   }
@@ -2545,7 +2547,7 @@ ig4_status launch_add_norm_grad(int M, int D, const void *s, const float *g, flo
                    g, eps, dyp, dsp, dxp, pp, M, D);
   } else {
     if (p.smem > DEFAULT_SMEM)
-      IG4_TRY(allow_smem(add_rms_norm_grad_kernel<XT, YT>, static_cast<int>(p.smem)));
+      IG4_TRY(allow_smem(add_rms_norm_grad_kernel<XT, YT>, ADDNORM_SM_SMEM));
     e = launch_pdl(add_rms_norm_grad_kernel<XT, YT>, dim3(p.grid), dim3(p.threads), p.smem, st, sp,
                    g, eps, dyp, dsp, dxp, pp, M, D, p.slots);
   }
@@ -2911,7 +2913,7 @@ ig4_status launch_grad_rows(const CUtensorMap &A0, const CUtensorMap &A1, const 
   IG4_TRY(device_info(&di));
   auto kern = grad_rows_kernel<DH>;
   const int smem = p.stages * grad_rows_stage_bytes(DH, p.nt) + 1024;
-  IG4_TRY(allow_smem(kern, smem));
+  IG4_TRY(allow_smem(kern, GRAD_ROWS_SMEM));
   if (launch_pdl(kern, dim3(std::min(p.items, di->sms)), dim3(GEMM_THREADS), smem, st, A0, A1, B, p,
                  static_cast<const __nv_bfloat16 *>(du), static_cast<__nv_bfloat16 *>(out),
                  part) != cudaSuccess)

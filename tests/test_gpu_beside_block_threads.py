@@ -75,3 +75,9 @@ def run_in_threads(ig4, calls, times):
                                     (swiglu_backward, 200), (matvec, 3), (rotate, 3)])
 def test_the_first_call_of_a_thread(ig4, make, M):
     run_in_threads(ig4, [make(ig4, M)], 1)
+
+
+@pytest.mark.parametrize("make,sizes", [(norm, (1, 500)), (norm_backward, (1, 500)),
+                                        (swiglu_backward, (17, 128))])
+def test_two_threads_with_sizes_of_different_shared_memory(ig4, make, sizes):
+    run_in_threads(ig4, [make(ig4, M) for M in sizes], 8000)
