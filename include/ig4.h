@@ -335,10 +335,11 @@ ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long
  * sequences) with bf16 activations: no activation is quantised,
  *   out[m][n] = w_scale[n] * sum_k x[m][k] W(n,k) (+ bias[n]),
  *   W(n,k) = e4m3(w_sf[n][k/16]) * e2m1(w_code[n][k]),
- * products exact, sums fp32, x to 2^-22 of the largest element of its row or less
- * (elements from 2^-13 of it on are exact).  A row of x that holds an infinity or a
- * NaN comes out as NaN.  x bf16 [M][K]; w_codes [N][K/2]; w_sf packed by
- * ig4_nvfp4_pack_scales, no scale negative; w_scale [N],
+ * products exact, sums fp32: every element of x counts with all its bits, an infinity
+ * or a NaN as in the formula.  (Elements more than 2^26 times smaller than the largest of
+ * their part of the row, infinities and NaN are multiplied one by one: a row with
+ * thousands of them takes many times longer.)  x bf16 [M][K]; w_codes [N][K/2]; w_sf
+ * packed by ig4_nvfp4_pack_scales (UE4M3: no scale is negative); w_scale [N],
  * bias [N] (or NULL) fp32; out [M][N] fp32 or bf16 (out_dtype).
  * ig4_nvfp4_swiglu_matvec: the gated pair, u_out[m][i] = silu(g) * up bf16 [M][I]
  * with g and up the two products.  1 <= M <= 8, N, I >= 1 (any), K % 64 == 0,

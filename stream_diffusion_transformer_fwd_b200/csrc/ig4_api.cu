@@ -2679,25 +2679,30 @@ constexpr int GRAD_SMS = 148;  // sm_100a
 // clusters that run at once take the row tiles in rounds; in clocks: a round
 // streams a CTA's k-blocks (200 each) and hands its sums over (2500 between CTAs,
 // 1000 without; hidden behind the next round's streaming where that is longer);
-// in front of the first, the digits (60 per row and k-block).
+// in front of the first, the digits (1200 for a row and k-block of each digit warp).
 struct MatvecPlan {
   int cluster, stages;
 };
 MatvecPlan matvec_plan(int M, int mats, int nkb, long tiles, const int (&fit)[MATVEC_MAX_CLUSTER + 1]) {
   MatvecPlan best{};
   long best_cost = 0;
-  for (int c = 1; c <= MATVEC_MAX_CLUSTER && c <= nkb; ++c) {
-    const int kbs = (nkb + c - 1) / c, each = (128 + c - 1) / c;
-    const int left = MATVEC_SMEM - 1024 - matvec_digit_bytes(M, kbs) - matvec_sum_bytes(M, mats, c, each);
-    const int stages = std::min(MATVEC_MAX_STAGES, left / MATVEC_STAGE_BYTES);
-    if (kbs * M > MATVEC_MAX_ITEMS * MATVEC_DIGIT_WARPS || stages < MATVEC_MIN_STAGES || fit[c] < 1) continue;
-    const long rounds = (tiles + fit[c] - 1) / fit[c];
-    const long stream = 200L * kbs * mats, sums = c > 1 ? 2500 : 1000;
-    const long cost = (rounds - 1) * std::max(stream, sums) + stream + sums + 60L * kbs * M;
-    if (best.cluster == 0 || cost < best_cost) {
-      best = {c, stages};
-      best_cost = cost;
+  // (long slices of many rows leave room for fewer stages than the loads would like)
+  for (int least : {std::max(MATVEC_MIN_STAGES, matvec_slots(M)), matvec_slots(M)}) {
+    for (int c = 1; c <= MATVEC_MAX_CLUSTER && c <= nkb; ++c) {
+      const int kbs = (nkb + c - 1) / c, each = (128 + c - 1) / c;
+      const int left = MATVEC_SMEM - 1024 - matvec_digit_bytes(M, kbs) - matvec_sum_bytes(M, mats, c, each);
+      const int stages = std::min(matvec_max_stages(M), left / MATVEC_STAGE_BYTES);
+      if (kbs * M > MATVEC_MAX_ITEMS * MATVEC_DIGIT_WARPS || stages < least || fit[c] < 1) continue;
+      const long rounds = (tiles + fit[c] - 1) / fit[c];
+      const long stream = 200L * kbs * mats, sums = c > 1 ? 2500 : 1000;
+      const long cost = (rounds - 1) * std::max(stream, sums) + stream + sums +
+                        1200L * ((kbs * M + MATVEC_DIGIT_WARPS - 1) / MATVEC_DIGIT_WARPS);
+      if (best.cluster == 0 || cost < best_cost) {
+        best = {c, stages};
+        best_cost = cost;
+      }
     }
+    if (best.cluster > 0) break;
   }
   return best;
 }
@@ -2748,8 +2753,8 @@ ig4_status launch_matvec(int M, int N, int K, const void *x, const MatvecWeights
     t1 = t0;
   const int clusters = std::min(tiles, fit[p.cluster]);
   const int each = (128 + p.cluster - 1) / p.cluster;
-  const MatvecArgs a{static_cast<const __nv_bfloat16 *>(x), {w0.sf, w1.sf}, {w0.scale, w1.scale},
-                     bias, out, M, N, K, tiles, p.cluster, clusters, p.stages,
+  const MatvecArgs a{static_cast<const __nv_bfloat16 *>(x), {w0.codes, w1.codes}, {w0.sf, w1.sf},
+                     {w0.scale, w1.scale}, bias, out, M, N, K, tiles, p.cluster, clusters, p.stages,
                      ((K + 255) / 256 + p.cluster - 1) / p.cluster, each, matvec_divider(M),
                      matvec_divider(p.cluster), matvec_divider(each)};
   attr[1].val.clusterDim.x = p.cluster;
