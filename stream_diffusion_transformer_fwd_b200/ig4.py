@@ -215,7 +215,7 @@ def _refuse(where: str):
 
 def _device_of(where: str, t) -> int:
     """Index of the tensor's device, which has to be the current one."""
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t is None or not t.is_cuda or t.get_device() != torch.cuda.current_device():
         _refuse(where)
     return t.get_device()
 
@@ -571,7 +571,7 @@ def ig4_add_rms_norm(x, r, g, eps, s_out, y_out, y_scale_out=None, y_sf_out=None
     name = "ig4_add_rms_norm"
     dev = _device_of(name, x)
     shape, dt, n = x.shape, x.dtype, x.numel()
-    if n == 0 or not shape:
+    if n == 0 or not shape or y_out is None:
         _refuse(name)
     D = shape[-1]
     M = n // D
@@ -598,7 +598,7 @@ def ig4_add_rms_norm_backward(s, g, eps, dy, ds, dx_out, dg_out, workspace=None,
     name = "ig4_add_rms_norm_backward"
     dev = _device_of(name, s)
     shape, dt, n = s.shape, s.dtype, s.numel()
-    if n == 0 or not shape:
+    if n == 0 or not shape or dy is None or dx_out is None:
         _refuse(name)
     D = shape[-1]
     M = n // D
@@ -622,7 +622,7 @@ def _heads(where: str, dev: int, t, B: int, L: int, d: int, dt):
     """ig4_heads of a [B, L, H, d] view (elements of a head contiguous)."""
     shape, strides = t.shape, t.stride()
     if t.get_device() != dev or t.dtype != dt or len(shape) != 4 or shape[0] != B or \
-            shape[1] != L or shape[3] != d or (d > 1 and strides[3] != 1):
+            shape[1] != L or shape[3] != d or (d > 1 and strides[3] != 1) or shape[2] > _INT_MAX:
         _refuse(where)
     # a dimension of one element is never stepped over, whatever its stride says
     return _pack_heads(t.data_ptr(), shape[2], strides[0] if B > 1 else 0,
@@ -636,16 +636,19 @@ def ig4_mrope_rotate(q, k, pos, theta, sections, q_out, k_out, rotary_dim=None, 
     defaults to twice the sum of sections; inverse=True rotates back (the gradient)."""
     name = "ig4_mrope_rotate"
     dev = _device_of(name, q)
-    if q.dim() != 4 or (k is None) != (k_out is None):
+    if q.dim() != 4 or pos is None or q_out is None or (k is None) != (k_out is None):
         _refuse(name)
     (B, L, _, d), dt = q.shape, q.dtype
     shared = pos.dim() == 2
-    s0, s1, s2 = sections
+    try:
+        s0, s1, s2 = sections
+        rotary = _pack_rotary(B, L, d, 2 * (s0 + s1 + s2) if rotary_dim is None else rotary_dim,
+                              theta, s0, s1, s2, bool(interleaved), bool(adjacent), bool(inverse),
+                              _DTYPE_CODE.get(dt, -1))
+    except (struct.error, TypeError, ValueError, OverflowError):  # not three small numbers
+        _refuse(name)
     _check(_lib.ig4_mrope_rotate(
-        _pack_rotary(B, L, d, 2 * (s0 + s1 + s2) if rotary_dim is None else rotary_dim, theta,
-                     s0, s1, s2, bool(interleaved), bool(adjacent), bool(inverse),
-                     _DTYPE_CODE.get(dt, -1)),
-        _dense(name, dev, pos, (3, L) if shared else (B, 3, L), torch.int32),
+        rotary, _dense(name, dev, pos, (3, L) if shared else (B, 3, L), torch.int32),
         0 if shared else 3 * L, _heads(name, dev, q, B, L, d, dt),
         _heads(name, dev, q_out, B, L, d, dt),
         None if k is None else _heads(name, dev, k, B, L, d, dt),
@@ -656,7 +659,8 @@ def ig4_mrope_rotate(q, k, pos, theta, sections, q_out, k_out, rotary_dim=None, 
 def _nvfp4(where: str, dev: int, codes, sf, scale, K: int) -> tuple:
     """Addresses of NVFP4 weights [N, K]: codes uint8 [N, K/2], packed scales, fp32 scale [N]."""
     N = codes.shape[0]
-    if sf.numel() < (N + 127) // 128 * 128 * K // 16:
+    if sf is None or scale is None or max(N, K) > _INT_MAX or \
+            sf.numel() < (N + 127) // 128 * 128 * K // 16:
         _refuse(where)
     return (_dense(where, dev, codes, (N, K // 2), torch.uint8),
             _dense(where, dev, sf, sf.shape, torch.uint8),
@@ -667,7 +671,7 @@ def ig4_nvfp4_matvec(x, w_codes, w_sf, w_scale, bias, out, stream=None):
     """out [M, N] (fp32 or bf16) = x [M, K] (bf16, M <= 8) times NVFP4 weights (+ bias)."""
     name = "ig4_nvfp4_matvec"
     dev = _device_of(name, x)
-    if x.dim() != 2 or w_codes.dim() != 2:
+    if x.dim() != 2 or w_codes is None or w_codes.dim() != 2 or out is None:
         _refuse(name)
     (M, K), N = x.shape, w_codes.shape[0]
     _check(_lib.ig4_nvfp4_matvec(
@@ -682,7 +686,8 @@ def ig4_nvfp4_swiglu_matvec(x, gate_codes, gate_sf, gate_scale, up_codes, up_sf,
     """u_out [M, I] bf16 = silu(x Wg^T) * (x Wu^T), x [M, K] bf16, M <= 8, NVFP4 weights."""
     name = "ig4_nvfp4_swiglu_matvec"
     dev = _device_of(name, x)
-    if x.dim() != 2 or gate_codes.dim() != 2 or up_codes.shape != gate_codes.shape:
+    if x.dim() != 2 or gate_codes is None or up_codes is None or gate_codes.dim() != 2 or \
+            up_codes.shape != gate_codes.shape:
         _refuse(name)
     (M, K), I = x.shape, gate_codes.shape[0]
     _check(_lib.ig4_nvfp4_swiglu_matvec(
@@ -702,7 +707,7 @@ def ig4_swiglu_backward(h, w_gate, w_up, du, dh_out, dw_gate_out, dw_up_out, wor
     wanted).  h [M, K], weights [I, K], du [M, I]."""
     name = "ig4_swiglu_backward"
     dev = _device_of(name, h)
-    if h.dim() != 2 or w_gate.dim() != 2:
+    if h.dim() != 2 or w_gate is None or w_gate.dim() != 2:
         _refuse(name)
     (M, K), I, b = h.shape, w_gate.shape[0], torch.bfloat16
     _check(_lib.ig4_swiglu_backward(
