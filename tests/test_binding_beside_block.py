@@ -1,5 +1,7 @@
-"""The binding of the operators beside the block: what it refuses before the library is called.
-Nothing here needs a GPU: host tensors stand in for the device's."""
+"""The binding of the operators beside the block: what it refuses before the library is called, and
+the bytes that it hands over.  Nothing here needs a GPU: host tensors stand in for the device's."""
+
+import ctypes
 
 import pytest
 import torch
@@ -92,3 +94,24 @@ def test_more_weight_rows_than_an_int(ig4):
     args = list(arguments(ig4, "ig4_nvfp4_matvec"))
     args[1:4], args[5] = (Rows(), Many(), Scale()), Out()
     refuses(ig4, "ig4_nvfp4_matvec", args)
+
+def test_packed_structures_are_the_header_s(built):
+    """The bytes that ig4_mrope_rotate hands over against the C structures' own layout (which
+    test_abi_beside_block.py compares with the header)."""
+    rotary = built.Rotary(B=3, L=5, head_dim=7, rotary_dim=11, theta=1.5,
+                          sections=(ctypes.c_int * 3)(13, 17, 19), interleaved=23, adjacent=29,
+                          inverse=31, dtype=37)
+    packed = built._pack_rotary(3, 5, 7, 11, 1.5, 13, 17, 19, 23, 29, 31, 37)
+    assert len(packed) == ctypes.sizeof(built.Rotary)
+    assert bytes(rotary) == packed
+    heads = built.Heads(data=1 << 44, H=3, stride_b=1 << 41, stride_l=5, stride_h=7)
+    packed = built._pack_heads(1 << 44, 3, 1 << 41, 5, 7)
+    assert bytes(heads) == packed and len(packed) == ctypes.sizeof(built.Heads)
+
+
+def test_heads_are_packed_from_a_view(ig4):
+    buffer = torch.zeros(2, 6, 5, 64, dtype=B16)
+    view = buffer.transpose(1, 2)[:, :, 1:4]  # [2, 5, 3, 64]
+    got = ig4.Heads.from_buffer_copy(ig4._heads("heads", -1, view, 2, 5, 64, B16))
+    assert (got.data, got.H) == (view.data_ptr(), 3)
+    assert (got.stride_b, got.stride_l, got.stride_h) == view.stride()[:3]

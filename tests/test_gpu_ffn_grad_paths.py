@@ -23,3 +23,19 @@ def ig4(cuda_device):
 def test_partly_idle_warps(ig4, M, I, K):
     t = make(M, I, K)
     check(run(ig4, *t), *reference(*t))
+
+
+# dh of 90 and 85 tiles on 74 pairs: whole tiles and split ones together, some pairs with a second
+# item; the second shape's dG | dU exceeds 64 MiB, where tiles are walked in groups of ten rows of
+# them, with a group left over
+@pytest.mark.parametrize("M,I,K", [(1153, 512, 4608), (4200, 4096, 1216)])
+def test_whole_and_split_tiles_together(ig4, M, I, K):
+    t = make(M, I, K)
+    check(run(ig4, *t), *reference(*t))
+
+
+# more weight rows (columns) than 148 CTAs take at once: the few-token products' second item each
+@pytest.mark.parametrize("M,I,K", [(17, 19072, 128), (17, 128, 19072), (70, 38016, 64)])
+def test_more_weight_rows_than_the_device_takes_at_once(ig4, M, I, K):
+    t = make(M, I, K)
+    check(run(ig4, *t), *reference(*t))
