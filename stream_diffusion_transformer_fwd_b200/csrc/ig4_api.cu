@@ -3104,12 +3104,13 @@ ig4_status ig4_mrope_rotate(const ig4_rotary *rot, const int32_t *pos, long long
   for (RotateHeads &t : a.t) {
     const int nh = (t.H + a.hs - 1) / a.hs;
     t.turn = rotate_walk_plan(t.H ? units : 0, nh, a.tt);
-    // the elements past the rotary ones: walks over equal runs of at most 256
-    // vectors (none in place)
+    // the elements past the rotary ones: walks over runs of at most 256 vectors (none in
+    // place), the last a little shorter.  (Runs of one length, which a prime number of
+    // vectors splits into single ones: 4608 tokens of 18 heads of 1021, 2 of them rotary,
+    // took 788 us.)
     const int vecs = t.H && t.in != t.out ? (d - R) / V : 0;
-    int runs = 1;
-    while (vecs / runs > ROTATE_THREADS || vecs % runs) ++runs;
-    t.copy = rotate_walk_plan(vecs / runs, nh, a.tt);
+    const int runs = std::max(1, (vecs + ROTATE_THREADS - 1) / ROTATE_THREADS);
+    t.copy = rotate_walk_plan((vecs + runs - 1) / runs, nh, a.tt);
   }
   const dim3 grid(static_cast<unsigned>(tiles), a.hs);
   cudaStream_t st = as_stream(stream);

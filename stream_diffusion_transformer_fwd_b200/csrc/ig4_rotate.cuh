@@ -159,19 +159,19 @@ struct RotStep {
   }
 };
 
-// Visits every (token < nt, head < nh) of the thread's unit: begin(token, unit)
-// once per token, then load(value, address) of NB heads before finish(value,
+// Visits every (token < nt, head < nh) of the thread's unit, if that is below `units`:
+// begin(token, unit) once per token, then load(value, address) of NB heads before finish(value,
 // address) of the first (an output may be its input, so the compiler cannot move loads
 // above stores by itself).
 template <int NB, typename Raw, typename T, typename Begin, typename Load, typename Finish>
 __device__ __forceinline__ void rotate_walk(const RotateWalk &k, const T *in, T *out,
                                             const long *base_in, const long *base_out, long in_h,
-                                            long out_h, int unit_size, int nt, int nh, Begin begin,
-                                            Load load, Finish finish) {
+                                            long out_h, int unit_size, int units, int nt, int nh,
+                                            Begin begin, Load load, Finish finish) {
   const int q = (static_cast<int>(threadIdx.x) * k.mu) >> 16;
   const int tk0 = (q * k.mh) >> 16;
   const int u = threadIdx.x - q * k.U, h0 = q - tk0 * k.HG;
-  if (tk0 >= k.TG) return;
+  if (tk0 >= k.TG || u >= units) return;
   const long din = k.HG * in_h, dout = k.HG * out_h;
   for (int tk = tk0; tk < nt; tk += k.TG) {
     begin(tk, u);
@@ -252,7 +252,8 @@ __global__ void __launch_bounds__(ROTATE_THREADS, ROTATE_CTAS)
     T *out = static_cast<T *>(t.out) + h0 * t.out_h;
     float cs[PU], sn[PU];
     rotate_walk<rotate_batch(sizeof(Vec)), Step>(
-        t.turn, in, out, base_in[w], base_out[w], t.in_h, t.out_h, ADJ && V == 1 ? 2 : V, nt, nh,
+        t.turn, in, out, base_in[w], base_out[w], t.in_h, t.out_h, ADJ && V == 1 ? 2 : V,
+        ROTATE_THREADS, nt, nh,
         [&](int tk, int u) {
 #pragma unroll
           for (int c = 0; c < PU / Q; ++c) {
@@ -272,11 +273,13 @@ __global__ void __launch_bounds__(ROTATE_THREADS, ROTATE_CTAS)
           v.turn(cs, sn);
           v.store(op, ADJ ? 1 : P);
         });
-    // elements past the rotary ones are copied (already there in place)
+    // elements past the rotary ones are copied (already there in place); the last run may
+    // be shorter
     if (t.copy.U > 0)
       for (int first = a.R; first < a.d; first += t.copy.U * V)
         rotate_walk<2 * rotate_batch(sizeof(Vec)), Vec>(
-            t.copy, in + first, out + first, base_in[w], base_out[w], t.in_h, t.out_h, V, nt, nh,
+            t.copy, in + first, out + first, base_in[w], base_out[w], t.in_h, t.out_h, V,
+            (a.d - first) / V, nt, nh,
             [](int, int) {}, [](Vec &v, const T *ip) { v.load(ip); },
             [](const Vec &v, T *op) { v.store(op); });
   }
