@@ -17,8 +17,8 @@
 // in registers, and thread 0 issues the row S further on.
 // D <= 512: a warp per row, the next row prefetched into registers.
 //
-// 9216 rows of 4608 bf16, sum and per-row E4M3 out: 51 to 55 us for 297 MB, 5.4 to
-// 5.8 TB/s (a plain copy 6.6); issue slots 65% busy.  2047 rows to MX8: 16.2 us, 3 of
+// 9216 rows of 4608 bf16, sum and per-row E4M3 out: 53 to 57 us for 297 MB, 5.2 to
+// 5.6 TB/s (a plain copy 6.6); issue slots 65% busy.  2047 rows to MX8: 16.2 us, 3 of
 // them launch and ramp.  Gradients of 4608 rows with dg: 31 us for the rows (170 MB,
 // 5.5 TB/s) and 4 to 5 us for the sum of the partial rows.  18000 rows of 512: 13.2 us.
 // One row: 2.3 us.
@@ -36,7 +36,13 @@ constexpr int ADDNORM_WARPS = 4;          // warps (rows) per CTA in that form
 constexpr int ADDNORM_NV = 2;             // vectors per thread
 constexpr int ADDNORM_MAX_THREADS = 512;  // CTA-per-row form: D <= 8192
 constexpr int ADDNORM_MAX_SLOTS = 8;
-// threads on an SM (the gradient kernel's register limit follows from its own)
+// Threads whose CTAs the grid counts for an SM.  The gradients' all fit: their register
+// limit follows from it (96 a thread, at which the fp32 forms spill 80 bytes).  The
+// forward's do not: at 54 to 64 registers 4 of the 5 CTAs at D = 4608 are resident, 3 for
+// MX8, and 4 to 6 of the warp form's 12 (77 to 110 registers); the others start as those
+// end.  Grids of the resident ones alone, with rings cut for them: 17.6 instead of 16.5 us
+// for 2047 rows of 4608 to MX8, 53 as before for 9216, E4M3 rows 14.0 instead of 14.9 and
+// 56.7 instead of 53 to 57, 18000 rows of 512 13.4 instead of 13.1.
 constexpr int ADDNORM_FWD_THREADS_PER_SM = 1536;
 constexpr int ADDNORM_BWD_THREADS_PER_SM = 640;
 

@@ -2425,7 +2425,7 @@ ig4_status ig4_selftest_timeout(int wait_us, void *stream) {
 }  // extern "C"
 
 // ------------------------------------------- operators beside the block
-// Residual addition + RMSNorm, rotary heads, SwiGLU gradients.
+// Residual addition + RMSNorm, rotary heads, few rows by NVFP4 weights, SwiGLU gradients.
 
 namespace {
 
@@ -2456,9 +2456,10 @@ inline size_t esize_of(int dt) { return dt == IG4_F32 ? 4 : (dt == IG4_BF16 ? 2 
 bool addnorm_sizes_ok(int M, int D) { return M >= 1 && D >= 8 && D % 8 == 0 && D <= 8192; }
 
 // Launch shape: a warp per row up to ADDNORM_WARP_D, else a CTA of as many
-// warps as cover the row with ADDNORM_NV vectors per thread, `ctas` of them on
-// an SM, walking the rows.  The ring gets the SM's shared memory in equal
-// parts, at least two slots (a row's inputs) per CTA.
+// warps as cover the row with ADDNORM_NV vectors per thread, `ctas` of them for
+// each SM (not all at once, see ADDNORM_FWD_THREADS_PER_SM), walking the rows.
+// The ring gets the SM's shared memory in equal parts, at least two slots (a
+// row's inputs) per CTA.
 struct AddNormPlan {
   bool warp;
   int threads, grid, slots;
@@ -2484,7 +2485,8 @@ AddNormPlan addnorm_plan(int M, int D, size_t slot_bytes, int sms, int threads_p
   p.smem = addnorm_smem(slot_bytes, p.slots);
   return p;
 }
-// (a warp of the gradients' warp-per-row form takes 128 to 165 registers a thread)
+// (the gradients' warp-per-row form takes 128 registers a thread, 4 CTAs on an SM; with an
+// fp32 s 154 to 165, 3 of the 4 planned)
 AddNormPlan addnorm_grad_plan(int M, int D, size_t slot_bytes, int sms) {
   return addnorm_plan(M, D, slot_bytes, sms,
                       D <= ADDNORM_WARP_D ? 512 : ADDNORM_BWD_THREADS_PER_SM);

@@ -18,10 +18,10 @@
 // rows per 128-byte-swizzled 1 KB atom), so nothing is transposed in memory.
 // Tokens past M read as zero from the TMA loads and add nothing.
 //
-// 12288 x 4608 weights: 4608 tokens (3131 GFLOP) 2.40 to 2.46 ms, 1.27 to 1.30 PFLOP/s
-// at the power-capped clock, where cuBLAS sustains 1.39; 1152 tokens 0.61 to 0.71 ms,
+// 12288 x 4608 weights: 4608 tokens (3131 GFLOP) 2.40 to 2.54 ms, 1.23 to 1.30 PFLOP/s
+// at the power-capped clock, where cuBLAS sustains 1.39; 1152 tokens 0.61 to 0.72 ms,
 // depending on the GPU (recomputation, dh and dW 190 to 205 us each, tensor pipe 85, 89
-// and 78% of active cycles); 17 tokens, dh only, 79.4 us.
+// and 78% of active cycles); 17 tokens, dh only, 79 to 82 us.
 #pragma once
 
 #include "ig4_gemm.cuh"
@@ -404,8 +404,8 @@ __global__ void __launch_bounds__(256) grad_reduce_kernel(const GradPlan p, __nv
 //     is cut into shares, whose fp32 sums [share][M][K] grad_rows_reduce_kernel
 //     adds (none with one share).
 // 17 tokens at 12288 x 4608: 47 us for G, U (227 MB, 4.9 TB/s) and 41 us for dh (5.5 TB/s)
-// by themselves with a cold L2, 79.4 us together.  The bytes of the weights are read twice:
-// they do not stay in L2 (126 MB) between the products.
+// by themselves with a cold L2, 79 to 82 us together; 1 token 78, 64 90, 128 105.  The
+// weights (226 MB) are read by both products and do not fit L2 (126 MB) between them.
 struct GradRowsPlan {
   int tiles, R;      // output tiles; weight rows (DH: columns, 128) of each
   int nt;            // tokens rounded up to 16

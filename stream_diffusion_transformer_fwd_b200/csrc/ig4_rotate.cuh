@@ -18,7 +18,8 @@
 //
 // 2 x 4608 tokens, 18 + 18 bf16 heads of 256 (64 pairs), strided in and out: 63 us for
 // 340 MB, 5.4 TB/s, 82% of a plain copy.  8 single tokens of as many heads: 4.8 us.
-// 2032 tokens of 16 + 4 fp32 heads of 128, adjacent pairs: 10.9 us, 3.8 TB/s.
+// 2032 tokens of 16 + 4 fp32 heads of 128, adjacent pairs: 10.9 us, 3.8 TB/s (508 CTAs,
+// fewer than the SMs hold, and none's loads start before its table is done).
 #pragma once
 
 #include "ig4_ptx.cuh"
@@ -31,8 +32,9 @@ constexpr int ROTATE_CTAS = 4;         // on an SM (64 registers a thread)
 constexpr int ROTATE_MAX_TOKENS = 8;  // of a CTA
 constexpr int ROTATE_TABLE = 1024;    // pairs in a CTA's table, all tokens
 // Heads whose loads a thread has in flight: wide vectors fill the 64 registers
-// with two (four spill and take twice the time), narrow ones need more loads
-// for the same bytes.
+// with two (28 bytes spill for halves of bf16 heads; four take twice the time),
+// narrow ones need more loads for the same bytes (three: 32 bytes spill at 8-byte
+// vectors of bf16, 24 of fp32).
 __host__ __device__ constexpr int rotate_batch(int bytes) { return bytes == 16 ? 2 : 3; }
 
 // Threads of a walk: thread i takes unit i % U, of heads i / U % HG, + HG, ..
